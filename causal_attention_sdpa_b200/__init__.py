@@ -10,6 +10,7 @@ Entry points (same names as the C ABI, see include/gpt_attn.h):
   gpt_attn_bwd(q, k, v, o, lse, dO, scale=None, window=0, dq=None, dk=None, dv=None,
                workspace=None, stream=None) -> (dq, dk, dv)
   gpt_attn_bwd_workspace_bytes(B, H, T, D) -> int
+  gpt_attn_fwd_sinks / gpt_attn_bwd_sinks: a sliding window with first tokens that stay visible
   gpt_attn_check(stream=None) -> int
   gpt_attn_status_string(status) -> str
 Tensors are bf16 contiguous [B, H, T, D] on the GPU; lse is fp32 [B, H, T].
@@ -38,7 +39,8 @@ EXPORTED = ("gpt_attn_fwd", "gpt_attn_bwd", "gpt_attn_bwd_workspace_bytes", "gpt
             "gpt_attn_bwd_grads", "gpt_attn_bwd_dq_convert", "gpt_attn_check", "gpt_attn_status_string",
             "gpt_attn_debug_wait_timeout", "gpt_attn_bwd_noalloc", "gpt_attn_tmap_cache_stats",
             "gpt_attn_fwd_ex", "gpt_attn_bwd_ex", "gpt_attn_decode", "gpt_attn_decode_workspace_bytes",
-            "gpt_attn_debug_skip_load", "gpt_attn_qk_prologue_fwd", "gpt_attn_qk_prologue_bwd")
+            "gpt_attn_debug_skip_load", "gpt_attn_qk_prologue_fwd", "gpt_attn_qk_prologue_bwd",
+            "gpt_attn_fwd_sinks", "gpt_attn_bwd_sinks", "gpt_attn_bwd_sinks_workspace_bytes")
 
 
 class GptAttnStrides(ctypes.Structure):
@@ -102,6 +104,12 @@ def lib() -> ctypes.CDLL:
         L.gpt_attn_fwd_ex.restype = i
         L.gpt_attn_bwd_ex.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, f, mp, lp, vp, sz, vp]
         L.gpt_attn_bwd_ex.restype = i
+        L.gpt_attn_fwd_sinks.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, f, mp, i, lp, vp]
+        L.gpt_attn_fwd_sinks.restype = i
+        L.gpt_attn_bwd_sinks.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, f, mp, i, lp, vp, sz, vp]
+        L.gpt_attn_bwd_sinks.restype = i
+        L.gpt_attn_bwd_sinks_workspace_bytes.argtypes = [i, i, i, i, i, i]
+        L.gpt_attn_bwd_sinks_workspace_bytes.restype = sz
         L.gpt_attn_decode_workspace_bytes.argtypes = [i, i, i, i, i]
         L.gpt_attn_decode_workspace_bytes.restype = sz
         L.gpt_attn_decode.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, f, i, vp, sz, vp]
@@ -313,6 +321,98 @@ def gpt_attn_bwd_ex(q, k, v, o, lse, dO, scale=None, window=0, head_windows=None
     del keep
     if rc != GPT_ATTN_OK:
         raise GptAttnError(rc, "gpt_attn_bwd_ex")
+    return dq, dk, dv
+
+
+def _launch(what, device, stream, *args):
+    """Calls the entry point `what` with `args` and the stream, the tensors' device being current."""
+    import torch
+    fn = getattr(lib(), what)
+    if device.index == torch.cuda.current_device():
+        rc = fn(*args, _stream_handle(stream))
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, _stream_handle(stream))
+    if rc != GPT_ATTN_OK:
+        raise GptAttnError(rc, what)
+
+
+def _check_tensor(name, t, dtype, shape, device):
+    """A contiguous CUDA tensor of the given type and shape on `device`."""
+    if t.dtype != dtype or t.device != device or not t.is_cuda or tuple(t.shape) != tuple(shape) or \
+            not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {str(dtype)[6:]} tensor of shape {tuple(shape)} on {device}")
+
+
+def _check_workspace(t, device):
+    if not t.is_cuda or t.device != device or not t.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+
+
+def _check_sinks_call(q, doc_start, head_windows, lse, views):
+    """The arguments of a call with sinks; returns (B, H, T, D)."""
+    import torch
+    if q.dim() != 4:
+        raise ValueError("q must be a CUDA bf16 [B, H, T, D] view")
+    B, H, T, D = q.shape
+    for n, t in views:
+        _check_view(n, t, q.shape)
+        if t.device != q.device:
+            raise ValueError(f"{n} must be on {q.device}")
+    if lse is not None:
+        _check_tensor("lse", lse, torch.float32, (B, H, T), q.device)
+    if doc_start is not None:
+        _check_tensor("doc_start", doc_start, torch.int32, (B, T), q.device)
+    if head_windows is not None and len(head_windows) != H:
+        raise ValueError(f"head_windows needs {H} entries")
+    return B, H, T, D
+
+
+def gpt_attn_fwd_sinks(q, k, v, window=0, sinks=0, scale=None, head_windows=None, doc_start=None, o=None, lse=None,
+                       stream=None):
+    """Sliding-window forward in which the first `sinks` tokens of each document (of the row without
+    doc_start) stay visible: query i sees key j iff doc_start[i] <= j <= i and (i - j < window or
+    j - doc_start[i] < sinks).  Views and the other arguments as for gpt_attn_fwd_ex; returns (o, lse)."""
+    import torch
+    B, H, T, D = _check_sinks_call(q, doc_start, head_windows, lse, (("q", q), ("k", k), ("v", v)))
+    scale = 1.0 / math.sqrt(D) if scale is None else scale
+    o = torch.empty((B, H, T, D), dtype=q.dtype, device=q.device) if o is None else o
+    _check_sinks_call(q, None, None, None, (("o", o),))
+    lse = torch.empty((B, H, T), dtype=torch.float32, device=q.device) if lse is None else lse
+    m, keep = _mask(H, window, head_windows, doc_start)
+    lay = _layout(q=q, k=k, v=v, o=o, dO=o, dq=o, dk=o, dv=o)
+    _launch("gpt_attn_fwd_sinks", q.device, stream, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, H, T, D,
+            float(scale), ctypes.byref(m), int(sinks), _byref(lay))
+    return o, lse
+
+
+def gpt_attn_bwd_sinks_workspace_bytes(B, H, T, D, window=0, sinks=0) -> int:
+    """Bytes of workspace of gpt_attn_bwd_sinks (window: the largest of the call's windows)."""
+    return int(lib().gpt_attn_bwd_sinks_workspace_bytes(int(B), int(H), int(T), int(D), int(window), int(sinks)))
+
+
+def gpt_attn_bwd_sinks(q, k, v, o, lse, dO, window=0, sinks=0, scale=None, head_windows=None, doc_start=None,
+                       dq=None, dk=None, dv=None, workspace=None, stream=None):
+    """Backward pass of gpt_attn_fwd_sinks under the same mask; returns (dq, dk, dv)."""
+    import torch
+    B, H, T, D = _check_sinks_call(q, doc_start, head_windows, lse,
+                                   (("q", q), ("k", k), ("v", v), ("o", o), ("dO", dO)))
+    scale = 1.0 / math.sqrt(D) if scale is None else scale
+    mk = lambda: torch.empty((B, H, T, D), dtype=q.dtype, device=q.device)
+    dq = mk() if dq is None else dq
+    dk = mk() if dk is None else dk
+    dv = mk() if dv is None else dv
+    _check_sinks_call(q, None, None, None, (("dq", dq), ("dk", dk), ("dv", dv)))
+    if workspace is None:
+        top = max(head_windows) if head_windows is not None else window
+        workspace = torch.empty(max(gpt_attn_bwd_sinks_workspace_bytes(B, H, T, D, top, sinks), 16),
+                                dtype=torch.uint8, device=q.device)
+    _check_workspace(workspace, q.device)
+    m, keep = _mask(H, window, head_windows, doc_start)
+    lay = _layout(q=q, k=k, v=v, o=o, dO=dO, dq=dq, dk=dk, dv=dv)
+    _launch("gpt_attn_bwd_sinks", q.device, stream, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dO),
+            _ptr(dq), _ptr(dk), _ptr(dv), B, H, T, D, float(scale), ctypes.byref(m), int(sinks), _byref(lay),
+            _ptr(workspace), workspace.numel() * workspace.element_size())
     return dq, dk, dv
 
 

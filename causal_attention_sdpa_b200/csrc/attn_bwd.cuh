@@ -64,8 +64,17 @@ struct BwdParams {
 };
 
 // Last query tile that sees key tile kt of head bh (window W).
-__device__ __forceinline__ int bwd_last_tile(const BwdParams& p, int bh, int kt, int W) {
-    return p.last_qt ? __ldg(p.last_qt + (size_t)bh * p.n_tiles + kt) : bwd_last_query_tile(kt, p.n_tiles, W);
+template <typename Mask>
+__device__ __forceinline__ int bwd_last_tile(const BwdParams& p, const Mask& mask, int bh, int kt, int W) {
+    if (p.last_qt) return __ldg(p.last_qt + (size_t)bh * p.n_tiles + kt);
+    if constexpr (Mask::kSinks) return bwd_last_query_tile_sinks(kt, p.n_tiles, W, mask.sinks);
+    return bwd_last_query_tile(kt, p.n_tiles, W);
+}
+
+// With sinks: whether key `key` of head bh is a sink, hence seen by every later query of its
+// document whatever the window.
+__device__ __forceinline__ bool is_sink(const SinkMask& mask, int bh, int T, int key) {
+    return key < T && key - mask.doc_of(bh, T, key) < mask.sinks;
 }
 
 template <int D>
@@ -123,13 +132,15 @@ struct BwdSmem {
 // bound of visible keys (INT_MAX past T) and, from the first row of each key tile,
 // the last query tile that sees the tile: the first rows' lower bounds do not
 // decrease, so the query tiles that see a key tile are the ones up to the last
-// whose first row's lower bound is at or before the tile's last key.
-template <int D>
+// whose first row's lower bound is at or before the tile's last key.  With sinks the
+// bound written is the start of the row's document alone: whether the window or the
+// sinks let a query see a key of its document goes by the key (is_sink).
+template <int D, typename Mask>
 __global__ void __launch_bounds__(256)
 attn_bwd_prep_kernel(const __nv_bfloat16* __restrict__ o, const __nv_bfloat16* __restrict__ dout,
                      const float* __restrict__ lse, float* __restrict__ lse2, float* __restrict__ delta,
                      float* __restrict__ dq_acc, int* __restrict__ sched, int T, int T_pad,
-                     long long total_rows_pad, const MaskParams mask, int* __restrict__ lower2,
+                     long long total_rows_pad, const Mask mask, int* __restrict__ lower2,
                      int* __restrict__ last_qt, int n_tiles, const Strides o_str, const Strides do_str, int H) {
     constexpr int G = D / 8;
     if (blockIdx.x == 0 && threadIdx.x == 0) *sched = 0;
@@ -164,11 +175,19 @@ attn_bwd_prep_kernel(const __nv_bfloat16* __restrict__ o, const __nv_bfloat16* _
         lse2[row] = valid ? lse[bh * T + t] * 1.4426950408889634f : INFINITY;
         if (lower2) {
             const int W = mask_window(mask, (int)bh);
-            lower2[row] = valid ? mask_row_lower(mask, (int)bh, T, W, t) : INT_MAX;
-            if ((t & (kTile - 1)) == 0) {
-                const int b = (int)bh;
-                last_qt[bh * n_tiles + t / kTile] = bwd_last_query_tile_lb(
-                    t / kTile, n_tiles, [&](int qt) { return mask_row_lower(mask, b, T, W, qt * kTile); });
+            const int b = (int)bh;
+            if constexpr (Mask::kSinks) {
+                lower2[row] = valid ? mask.doc_of(b, T, t) : INT_MAX;
+                if ((t & (kTile - 1)) == 0)
+                    last_qt[bh * n_tiles + t / kTile] = bwd_last_query_tile_sinks_lb(
+                        t / kTile, n_tiles, mask.sinks,
+                        [&](int qt) { return mask_row_lower(mask, b, T, W, qt * kTile); },
+                        [&](int qt) { return mask.doc_of(b, T, qt * kTile); });
+            } else {
+                lower2[row] = valid ? mask_row_lower(mask, b, T, W, t) : INT_MAX;
+                if ((t & (kTile - 1)) == 0)
+                    last_qt[bh * n_tiles + t / kTile] = bwd_last_query_tile_lb(
+                        t / kTile, n_tiles, [&](int qt) { return mask_row_lower(mask, b, T, W, qt * kTile); });
             }
         }
     }
@@ -222,7 +241,7 @@ attn_bwd_serial_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
     const int k0 = kt * kTile;
     const int qt_lo = kt;
     const int W = mask.head_window(bh);
-    const int qt_hi = bwd_last_tile(p, bh, kt, W);
+    const int qt_hi = bwd_last_tile(p, mask, bh, kt, W);
     const int n_q = qt_hi - qt_lo + 1;
 
     if (threadIdx.x == 0) {
@@ -399,6 +418,8 @@ attn_bwd_serial_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
         const uint32_t t_lane = tmem + ((uint32_t)(wq * 32) << 16);
         const float sl2 = p.scale_log2;
         const bool doc = p.lower2 != nullptr;
+        bool sink = false;                          // this thread's key is seen past the window
+        if constexpr (Mask::kSinks) sink = is_sink(mask, bh, p.T, key);
         const uint32_t ds_row = smem_u32(sm.ds) + r * 128;
         bool ok = true;
         for (int it = 0; it < n_q; ++it) {
@@ -412,8 +433,8 @@ attn_bwd_serial_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
             // The tile needs the per-element mask if it holds the diagonal or some query of it
             // starts seeing keys after this key tile's first key (lower bounds do not decrease
             // down a tile, so its last row decides).
-            const bool need_mask =
-                (qt == kt) || (doc ? sm.lower[s][kTile - 1] > k0 : (W > 0 && q0 + kTile - 1 >= k0 + W));
+            const bool need_mask = (qt == kt) || (doc && sm.lower[s][kTile - 1] > k0) ||
+                                   ((!doc || Mask::kSinks) && W > 0 && q0 + kTile - 1 >= k0 + W);
             const float2* lse2 = reinterpret_cast<const float2*>(sm.lse2[s]);
             const float2* dlt = reinterpret_cast<const float2*>(sm.delta[s]);
 #pragma unroll 1
@@ -424,15 +445,24 @@ attn_bwd_serial_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                 tmem_wait_ld();
                 if (need_mask) {
                     const int c_lo = key - (q0 + c * 32);
+                    // visible query columns of this key: one range, compare + select per element
+                    // (a sink's has no upper end)
+                    const int c_hi = W > 0 && !sink ? key + W - 1 - (q0 + c * 32) : INT_MAX / 2;
                     if (doc) {
-                        // query q sees this key iff q >= key and lower(q) <= key
+                        // query q sees this key iff q >= key and lower(q) <= key (with sinks the
+                        // bound is the document's start, and the window goes by the range)
                         const int* lw = sm.lower[s] + c * 32;
+                        if constexpr (Mask::kSinks) {
+                            const uint32_t span = (uint32_t)(c_hi - c_lo);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            rs[e] = (e >= c_lo && lw[e] <= key) ? rs[e] : 0xff800000u;   // -inf: P = 0
+                            for (int e = 0; e < 32; ++e)
+                                rs[e] = ((uint32_t)(e - c_lo) <= span && lw[e] <= key) ? rs[e] : 0xff800000u;
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                rs[e] = (e >= c_lo && lw[e] <= key) ? rs[e] : 0xff800000u;   // -inf: P = 0
+                        }
                     } else {
-                        // visible query columns of this key: one range, compare + select per element
-                        const int c_hi = W > 0 ? key + W - 1 - (q0 + c * 32) : INT_MAX / 2;
                         const uint32_t span = (uint32_t)(c_hi - c_lo);
 #pragma unroll
                         for (int e = 0; e < 32; ++e)

@@ -99,7 +99,7 @@ __device__ __forceinline__ Bwd64Unit bwd64_unit(int u, const BwdParams& p, const
     Bwd64Unit w;
     list_item(u, p.BH, p.n_tiles, p.tail, w.bh, w.kt);
     w.W = mask.head_window(w.bh);
-    w.n_q = bwd_last_tile(p, w.bh, w.kt, w.W) - w.kt + 1;
+    w.n_q = bwd_last_tile(p, mask, w.bh, w.kt, w.W) - w.kt + 1;
     w.k0 = w.kt * kTile;
     w.qt_lo = w.kt;
     return w;
@@ -331,6 +331,8 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             const Bwd64Unit w = bwd64_unit(u, p, mask);
             const int W = w.W;
             const int key = w.k0 + r;
+            bool sink = false;                             // this thread's key is seen past the window
+            if constexpr (Mask::kSinks) sink = is_sink(mask, w.bh, p.T, key);
             for (int i = 0; i < w.n_q; ++i, ++g) {
                 const int s = g % kStages;
                 const int b = g & 1;
@@ -345,12 +347,13 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 // S^T and dP^T are read from TMEM while the first half is computed.
                 // The diagonal tile, and tiles some of whose queries start seeing keys after this
                 // key tile's first key (the tile's last row decides: lower bounds do not decrease).
-                const bool need_mask = (qt == w.kt) || (doc ? sm.lower[s][kTile - 1] > w.k0
-                                                            : (W > 0 && qt * kTile + kTile - 1 >= w.k0 + W));
+                const bool need_mask = (qt == w.kt) || (doc && sm.lower[s][kTile - 1] > w.k0) ||
+                                       ((!doc || Mask::kSinks) && W > 0 && qt * kTile + kTile - 1 >= w.k0 + W);
                 // Query columns that see this key form one range [c_lo, c_hi] (query >= key, and
-                // query < key + W under a window): blocked pairs get score -inf, hence P = dS = 0.
+                // query < key + W under a window, unless the key is a sink): blocked pairs get score
+                // -inf, hence P = dS = 0.
                 const int c_lo = key - qc0;
-                const int c_hi = W > 0 ? key + W - 1 - qc0 : INT_MAX / 2;
+                const int c_hi = W > 0 && !sink ? key + W - 1 - qc0 : INT_MAX / 2;
                 const uint32_t span = (uint32_t)(c_hi - c_lo);
                 const uint32_t row_a = smem_u32(sm.ds[b]) + h * 16384 + r * 128;
                 uint32_t xs[32], xd[32];
@@ -362,10 +365,18 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     if (need_mask) {
                         if (doc) {
                             // query column c sees this key iff c >= c_lo and lower(c) <= key
+                            // (with sinks lower(c) is the document's start, and the window goes by the range)
                             const int* lw = sm.lower[s] + h * 64 + hh * 32;
+                            if constexpr (Mask::kSinks) {
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                xs[e] = (hh * 32 + e >= c_lo && lw[e] <= key) ? xs[e] : 0xff800000u;
+                                for (int e = 0; e < 32; ++e)
+                                    xs[e] = ((uint32_t)(hh * 32 + e - c_lo) <= span && lw[e] <= key) ? xs[e]
+                                                                                                     : 0xff800000u;
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    xs[e] = (hh * 32 + e >= c_lo && lw[e] <= key) ? xs[e] : 0xff800000u;
+                            }
                         } else {
 #pragma unroll
                             for (int e = 0; e < 32; ++e)

@@ -66,6 +66,7 @@ struct WindowMask {
     // Lower bound of the keys query i sees (schedule.h row_lower).
     __device__ __forceinline__ int row_lower_of(int, int, int W, int i) const { return row_lower(i, W, 0); }
     static constexpr bool kDoc = false;
+    static constexpr bool kSinks = false;
 };
 
 constexpr int kMaxHeadWindows = 64;   // per-head windows travel in the kernel parameters
@@ -84,6 +85,18 @@ struct MaskParams {
         return row_lower(i, W, d);
     }
     static constexpr bool kDoc = true;
+    static constexpr bool kSinks = false;
+};
+
+// MaskParams with sinks: the first `sinks` tokens of a query's document stay visible past the
+// window.  The host clamps the windows and sinks to T, so sums of positions fit an int.
+struct SinkMask : MaskParams {
+    int sinks;
+    // First position of the document of query i (the last token's for rows past T).
+    __device__ __forceinline__ int doc_of(int bh, int T, int i) const {
+        return doc_start ? row_doc(i, __ldg(doc_start + (size_t)(bh / H) * T + (i < T ? i : T - 1))) : 0;
+    }
+    static constexpr bool kSinks = true;
 };
 
 __device__ __forceinline__ int mask_window(const MaskParams& m, int bh) { return m.head_window(bh); }
@@ -136,12 +149,26 @@ __device__ __forceinline__ void fwd_next_static_item(const FwdParams& p, int& k,
 // the eight softmax warps (one arrival per warp).
 constexpr int kFwdItemReaders = 3 + 8;
 
-// Key tiles [lo, hi] of query tile qt of head bh with window W.
+// Key tiles of query tile qt of head bh with window W.
 template <typename Mask>
-__device__ __forceinline__ void fwd_tile_range(const FwdParams& p, const Mask& m, int bh, int W, int qt, int& lo,
-                                               int& hi) {
-    fwd_key_range_lb(qt, m.row_lower_of(bh, p.T, W, qt * kTile), lo, hi);
+__device__ __forceinline__ FwdSpan fwd_span(const FwdParams& p, const Mask& m, int bh, int W, int qt) {
+    FwdSpan sp;
+    fwd_key_range_lb(qt, m.row_lower_of(bh, p.T, W, qt * kTile), sp.lo, sp.hi);
+    sp.s = sp.ns = 0;
+    if constexpr (Mask::kSinks) fwd_add_sinks(sp, m.doc_of(bh, p.T, qt * kTile), m.sinks);
+    return sp;
 }
+
+// Key tiles of the two query tiles of block qb.  The block visits a.ns sink tiles, then
+// [a.lo, b.hi]; position u of that sequence is tile block_tile(a, u).
+template <typename Mask>
+__device__ __forceinline__ void fwd_block_spans(const FwdParams& p, const Mask& m, int bh, int W, int qb, FwdSpan& a,
+                                                FwdSpan& b) {
+    a = fwd_span(p, m, bh, W, 2 * qb);
+    b = fwd_span(p, m, bh, W, 2 * qb + 1);
+    if constexpr (Mask::kSinks) fwd_fit_pair(a, b);
+}
+__device__ __forceinline__ int block_tiles(const FwdSpan& a, const FwdSpan& b) { return a.ns + b.hi - a.lo + 1; }
 
 template <int D>
 struct FwdCfg {
@@ -301,9 +328,9 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     clc_pending = true;
                 }
                 const int W = mask.head_window(bh);
-                int lo0, hi0, lo1, hi1;
-                fwd_tile_range(p, mask, bh, W, 2 * qb, lo0, hi0);
-                fwd_tile_range(p, mask, bh, W, 2 * qb + 1, lo1, hi1);
+                FwdSpan spa, spb;
+                fwd_block_spans(p, mask, bh, W, qb, spa, spb);
+                const int n_j = block_tiles(spa, spb);
                 const int qbuf = n_item % kQBufs;
                 if (n_item >= kQBufs &&
                     !(ok = mbar_wait(&sm.bar_q_empty[qbuf], ((n_item / kQBufs) - 1) & 1, ac)))
@@ -315,7 +342,8 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                         tma_load_4d(sm.q[qbuf][t] + b * 16384, &tm_q, &sm.bar_q[qbuf], b * 64, (2 * qb + t) * kTile,
                                     hh, bb);
                 ++n_item;
-                for (int j = lo0; j <= hi1; ++j, ++it) {
+                for (int u = 0; u < n_j; ++u, ++it) {
+                    const int j = spa.tile(u);
                     const int s = it % kStages;
                     const int n = it / kStages;
                     if (n > 0 && !(ok = mbar_wait(&sm.bar_kv_empty[s], (n - 1) & 1, ac))) break;
@@ -370,18 +398,19 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 int bh, qb;
                 if (!(ok = read_item(n, bh, qb)) || bh < 0) break;
                 const int W = mask.head_window(bh);
-                int lo[2], hi[2];
-                fwd_tile_range(p, mask, bh, W, 2 * qb, lo[0], hi[0]);
-                fwd_tile_range(p, mask, bh, W, 2 * qb + 1, lo[1], hi[1]);
+                FwdSpan sp[2];
+                fwd_block_spans(p, mask, bh, W, qb, sp[0], sp[1]);
+                const int n_j = block_tiles(sp[0], sp[1]);
                 const int qbuf = n_item % kQBufs;
                 if (!(ok = mbar_wait(&sm.bar_q[qbuf], (n_item / kQBufs) & 1, ac))) break;
                 const uint32_t q_addr0 = smem_u32(sm.q[qbuf][0]), q_addr1 = smem_u32(sm.q[qbuf][1]);
-                for (int j = lo[0]; ok && j <= hi[1]; ++j, ++it) {
+                for (int u = 0; ok && u < n_j; ++u, ++it) {
+                    const int j = sp[0].tile(u);
                     const int s = it % kStages;
                     if (!(ok = mbar_wait(&sm.bar_k[s], (it / kStages) & 1, ac))) break;
                     const uint32_t k_addr = smem_u32(sm.k[s]);
                     for (int t = 0; ok && t < 2; ++t) {
-                        if (j < lo[t] || j > hi[t]) continue;
+                        if (!sp[t].has(j)) continue;
                         if (ct[t] > 0) {
                             // S_t shares TMEM with what the previous tile still needs: the softmax
                             // copy of S (separate P) or, when P is written over S, the PV MMA that reads it.
@@ -406,7 +435,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                         // to this warp: made here, after the stage's load was waited for, it can
                         // only count towards this tile's phase.
                         for (int t = 0; t < 2; ++t)
-                            if (j < lo[t] || j > hi[t]) mma_commit(&sm.bar_kv_empty[s]);
+                            if (!sp[t].has(j)) mma_commit(&sm.bar_kv_empty[s]);
                     }
                 }
                 if (ok) mma_commit(&sm.bar_q_empty[qbuf]);    // the item's Q buffer may be reloaded
@@ -421,14 +450,15 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 int bh, qb;
                 if (!(ok = read_item(n, bh, qb)) || bh < 0) break;
                 const int W = mask.head_window(bh);
-                int lo0, hi0, lo1, hi1;
-                fwd_tile_range(p, mask, bh, W, 2 * qb, lo0, hi0);
-                fwd_tile_range(p, mask, bh, W, 2 * qb + 1, lo1, hi1);
-                const int lo = t ? lo1 : lo0, hi = t ? hi1 : hi0;
-                for (int j = lo0; ok && j <= hi1; ++j, ++it) {
+                FwdSpan spa, spb;
+                fwd_block_spans(p, mask, bh, W, qb, spa, spb);
+                const FwdSpan sp = t ? spb : spa;
+                const int n_j = block_tiles(spa, spb);
+                int i = 0;                               // PV tiles of this item
+                for (int u = 0; ok && u < n_j; ++u, ++it) {
+                    const int j = spa.tile(u);
                     const int s = it % kStages;
-                    if (j < lo || j > hi) continue;      // the S warp releases stage s for this warp
-                    const int i = j - lo;
+                    if (!sp.has(j)) continue;            // the S warp releases stage s for this warp
                     if (!(ok = mbar_wait(&sm.bar_v[s], (it / kStages) & 1, ac))) break;
                     if (!(ok = mbar_wait(&sm.bar_p_full[t], ct & 1, ac))) break;
                     // The item's first PV overwrites O: the previous item's epilogue must have read it.
@@ -442,6 +472,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     mma_commit(&sm.bar_o_done[t]);
                     mma_commit(&sm.bar_kv_empty[s]);
                     ++ct;
+                    ++i;
                 }
                 ++n_item;
             }
@@ -478,8 +509,14 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             const int qt = 2 * qb + t;
             const int i_abs = qt * kTile + row;
             const int W = mask.head_window(bh);
-            int lo, hi;
-            fwd_tile_range(p, mask, bh, W, qt, lo, hi);
+            FwdSpan sp;
+            if constexpr (Mask::kSinks) {
+                FwdSpan spa, spb;
+                fwd_block_spans(p, mask, bh, W, qb, spa, spb);
+                sp = t ? spb : spa;
+            } else {
+                sp = fwd_span(p, mask, bh, W, qt);
+            }
             // Visible keys of this row: [row_lo, i_abs].  A key tile needs the per-element mask if
             // it holds the diagonal or starts before the lower bound of the tile's last row (lower
             // bounds do not decrease down the tile).
@@ -487,10 +524,12 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             const int last_lo = mask.row_lower_of(bh, p.T, W, qt * kTile + kTile - 1);
             float m_used = -INFINITY;    // reference max of the exponentials (log2 units)
             float l = 0.f;               // running sum of 2^(x - m_used)
-            const int n_t = hi - lo + 1;
+            int row_d = 0;               // with sinks: first position of this row's document
+            if constexpr (Mask::kSinks) row_d = mask.doc_of(bh, p.T, i_abs);
+            const int n_t = sp.count();
             for (int i = 0; i < n_t; ++i) {
                 const int c = ct + i;    // phase index of this tile
-                const int j = lo + i;
+                const int j = sp.tile(i);
                 const int k0 = j * kTile;
                 if (!warp_wait(&sm.bar_s_full[t], c & 1, ac)) { ok = false; break; }
                 tc_fence_after();
@@ -514,9 +553,18 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     const int c_hi = i_abs - k0;
                     const int c_lo = row_lo - k0;
                     const uint32_t span = (uint32_t)(c_hi - c_lo);
+                    if constexpr (Mask::kSinks) {
+                        // and its sinks a second one, [k_lo, k_hi]
+                        const int k_lo = row_d - k0;
+                        const uint32_t k_span = (uint32_t)(min(row_d + mask.sinks - 1, i_abs) - row_d);
 #pragma unroll
-                    for (int e = 0; e < 128; ++e)
-                        s[e] = ((uint32_t)(e - c_lo) <= span) ? s[e] : -INFINITY;
+                        for (int e = 0; e < 128; ++e)
+                            s[e] = ((uint32_t)(e - c_lo) <= span || (uint32_t)(e - k_lo) <= k_span) ? s[e] : -INFINITY;
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 128; ++e)
+                            s[e] = ((uint32_t)(e - c_lo) <= span) ? s[e] : -INFINITY;
+                    }
                 }
                 // Exponentials.  After the first tile of a row the reference max m_used is finite and
                 // the exponentials start at once with it, the tile's own max being computed in the

@@ -187,6 +187,18 @@ int make_mask(MaskParams* m, const gpt_attn_mask* a, int H) {
 // True when every head shares one window and there are no document starts.
 bool plain_window(const MaskParams& m) { return !m.head_windows && !m.doc_start; }
 
+// The mask with sinks, every window and the sinks clamped to T (a window of T or more is causal:
+// nothing is out of its reach, so sinks add nothing).  Returns false when no head needs sinks.
+bool sink_mask(SinkMask* s, const MaskParams& m, int sinks, int H, int T) {
+    static_cast<MaskParams&>(*s) = m;
+    s->sinks = sinks < T ? sinks : T;
+    auto clamp = [&](int w) { return w > 0 && w < T ? w : 0; };
+    s->window = clamp(m.window);
+    bool any = !m.head_windows && s->window > 0;
+    for (int h = 0; m.head_windows && h < H; ++h) any |= (s->win[h] = clamp(m.win[h])) > 0;
+    return sinks > 0 && any;
+}
+
 MaskParams window_mask(int window, int H) {
     gpt_attn_mask a{window, nullptr, nullptr};
     MaskParams m;
@@ -196,7 +208,7 @@ MaskParams window_mask(int window, int H) {
 
 template <int D>
 int launch_fwd(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H, int T, float scale,
-               const MaskParams& mask, const Layout& L, cudaStream_t st) {
+               const MaskParams& mask, const Layout& L, cudaStream_t st, const SinkMask* sinks = nullptr) {
     const int BH = B * H;
     CUtensorMap mq, mk, mv, mo;
     if (!make_tmap_bf16(&mq, q, B, H, T, D, L.q) || !make_tmap_bf16(&mk, k, B, H, T, D, L.k) ||
@@ -228,7 +240,10 @@ int launch_fwd(const void* q, const void* k, const void* v, void* o, float* lse,
     }
     const size_t smem = sizeof(FwdSmem<D>) + 1024;
     const unsigned grid = stat ? (unsigned)(hpw * p.n_blocks) : (unsigned)((long long)BH * p.n_blocks);
-    if (plain_window(mask)) {
+    if (sinks) {
+        if (!set_smem(attn_fwd_kernel<D, SinkMask>, smem)) return GPT_ATTN_ERR_CUDA;
+        attn_fwd_kernel<D, SinkMask><<<grid, kFwdThreads, smem, st>>>(mq, mk, mv, mo, p, *sinks);
+    } else if (plain_window(mask)) {
         // Causal or one window for every head: the instantiation without per-head or document data.
         if (!set_smem(attn_fwd_kernel<D, WindowMask>, smem)) return GPT_ATTN_ERR_CUDA;
         attn_fwd_kernel<D, WindowMask><<<grid, kFwdThreads, smem, st>>>(mq, mk, mv, mo, p, WindowMask{mask.window});
@@ -280,8 +295,9 @@ int sm_count() {
     return n;
 }
 
+template <typename Mask>
 int launch_bwd_delta(const void* o, const float* lse, const void* dout, int B, int H, int T, int D, void* ws,
-                     const MaskParams& mask, const Layout& L, cudaStream_t st) {
+                     const Mask& mask, const Layout& L, cudaStream_t st) {
     const int BH = B * H;
     const WsLayout w = ws_layout(ws, BH, T, D);
     const long long rows = (long long)BH * w.T_pad;
@@ -291,19 +307,20 @@ int launch_bwd_delta(const void* o, const float* lse, const void* dout, int B, i
     const auto* do16 = static_cast<const __nv_bfloat16*>(dout);
     const bool doc = mask.doc_start != nullptr;
     if (D == 64)
-        attn_bwd_prep_kernel<64><<<grid, 256, 0, st>>>(o16, do16, lse, w.lse2, w.delta, w.dq_acc, w.sched, T,
-                                                        w.T_pad, rows, mask, doc ? w.lower2 : nullptr,
-                                                        w.last_qt, w.n_tiles, L.o, L.dO, H);
+        attn_bwd_prep_kernel<64, Mask><<<grid, 256, 0, st>>>(o16, do16, lse, w.lse2, w.delta, w.dq_acc, w.sched, T,
+                                                             w.T_pad, rows, mask, doc ? w.lower2 : nullptr,
+                                                             w.last_qt, w.n_tiles, L.o, L.dO, H);
     else
-        attn_bwd_prep_kernel<128><<<grid, 256, 0, st>>>(o16, do16, lse, w.lse2, w.delta, w.dq_acc, w.sched, T,
-                                                         w.T_pad, rows, mask, doc ? w.lower2 : nullptr,
-                                                         w.last_qt, w.n_tiles, L.o, L.dO, H);
+        attn_bwd_prep_kernel<128, Mask><<<grid, 256, 0, st>>>(o16, do16, lse, w.lse2, w.delta, w.dq_acc, w.sched, T,
+                                                              w.T_pad, rows, mask, doc ? w.lower2 : nullptr,
+                                                              w.last_qt, w.n_tiles, L.o, L.dO, H);
     return cudaGetLastError() == cudaSuccess ? GPT_ATTN_OK : GPT_ATTN_ERR_CUDA;
 }
 
 template <int D>
 int launch_bwd_grads(const void* q, const void* k, const void* v, const void* dout, void* dk, void* dv, int B,
-                     int H, int T, float scale, const MaskParams& mask, const Layout& L, void* ws, cudaStream_t st) {
+                     int H, int T, float scale, const MaskParams& mask, const Layout& L, void* ws, cudaStream_t st,
+                     const SinkMask* sinks = nullptr) {
     const int BH = B * H;
     const WsLayout w = ws_layout(ws, BH, T, D);
     CUtensorMap mq, mk, mv, mdo;
@@ -340,7 +357,10 @@ int launch_bwd_grads(const void* q, const void* k, const void* v, const void* do
         const size_t smem = sizeof(Bwd64Smem) + 1024;
         // persistent: one CTA per SM, work units taken from the counter in the workspace
         const unsigned pgrid = (unsigned)(units < sm_count() ? units : sm_count());
-        if (plain_window(mask)) {
+        if (sinks) {
+            if (!set_smem(attn_bwd_kernel<SinkMask>, smem)) return GPT_ATTN_ERR_CUDA;
+            attn_bwd_kernel<SinkMask><<<pgrid, kBwd64Threads, smem, st>>>(mq, mk, mv, mdo, mdq, mdk, mdv, p, *sinks);
+        } else if (plain_window(mask)) {
             if (!set_smem(attn_bwd_kernel<WindowMask>, smem)) return GPT_ATTN_ERR_CUDA;
             attn_bwd_kernel<WindowMask><<<pgrid, kBwd64Threads, smem, st>>>(mq, mk, mv, mdo, mdq, mdk, mdv, p,
                                                                           WindowMask{mask.window});
@@ -352,7 +372,10 @@ int launch_bwd_grads(const void* q, const void* k, const void* v, const void* do
         CUtensorMap mdq;
         if (!make_tmap_f32_acc(&mdq, w.dq_acc, BH, T, D)) return GPT_ATTN_ERR_CUDA;
         const size_t smem = sizeof(BwdSmem<D>) + 1024;
-        if (plain_window(mask)) {
+        if (sinks) {
+            if (!set_smem(attn_bwd_serial_kernel<D, SinkMask>, smem)) return GPT_ATTN_ERR_CUDA;
+            attn_bwd_serial_kernel<D, SinkMask><<<grid, kBwdThreads, smem, st>>>(mq, mk, mv, mdo, mdq, p, *sinks);
+        } else if (plain_window(mask)) {
             if (!set_smem(attn_bwd_serial_kernel<D, WindowMask>, smem)) return GPT_ATTN_ERR_CUDA;
             attn_bwd_serial_kernel<D, WindowMask><<<grid, kBwdThreads, smem, st>>>(mq, mk, mv, mdo, mdq, p,
                                                                                  WindowMask{mask.window});
@@ -519,8 +542,9 @@ using namespace gpt_attn;
 
 extern "C" {
 
-int gpt_attn_fwd_ex(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H, int T, int D,
-                    float scale, const gpt_attn_mask* mask, const gpt_attn_layout* layout, void* stream) {
+int gpt_attn_fwd_sinks(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H, int T, int D,
+                       float scale, const gpt_attn_mask* mask, int sinks, const gpt_attn_layout* layout,
+                       void* stream) {
     if (!q || !k || !v || !o || !lse) return GPT_ATTN_ERR_NULL;
     int sc = check_shape(B, H, T, D);
     if (sc != GPT_ATTN_OK) return sc;
@@ -530,8 +554,15 @@ int gpt_attn_fwd_ex(const void* q, const void* k, const void* v, void* o, float*
     Layout L;
     if ((sc = make_layout(&L, layout, H, T, D)) != GPT_ATTN_OK) return sc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return D == 64 ? launch_fwd<64>(q, k, v, o, lse, B, H, T, scale, m, L, st)
-                   : launch_fwd<128>(q, k, v, o, lse, B, H, T, scale, m, L, st);
+    SinkMask sm;
+    const SinkMask* sp = sink_mask(&sm, m, sinks, H, T) ? &sm : nullptr;
+    return D == 64 ? launch_fwd<64>(q, k, v, o, lse, B, H, T, scale, m, L, st, sp)
+                   : launch_fwd<128>(q, k, v, o, lse, B, H, T, scale, m, L, st, sp);
+}
+
+int gpt_attn_fwd_ex(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H, int T, int D,
+                    float scale, const gpt_attn_mask* mask, const gpt_attn_layout* layout, void* stream) {
+    return gpt_attn_fwd_sinks(q, k, v, o, lse, B, H, T, D, scale, mask, 0, layout, stream);
 }
 
 int gpt_attn_fwd(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H, int T, int D,
@@ -585,9 +616,15 @@ int gpt_attn_bwd_dq_convert(void* dq, int B, int H, int T, int D, float scale, v
                              static_cast<cudaStream_t>(stream));
 }
 
-int gpt_attn_bwd_ex(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dO,
-                    void* dq, void* dk, void* dv, int B, int H, int T, int D, float scale, const gpt_attn_mask* mask,
-                    const gpt_attn_layout* layout, void* workspace, size_t workspace_bytes, void* stream) {
+size_t gpt_attn_bwd_sinks_workspace_bytes(int B, int H, int T, int D, int window, int sinks) {
+    (void)window;
+    (void)sinks;
+    return gpt_attn_bwd_workspace_bytes(B, H, T, D);
+}
+
+int gpt_attn_bwd_sinks(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dO,
+                       void* dq, void* dk, void* dv, int B, int H, int T, int D, float scale, const gpt_attn_mask* mask,
+                       int sinks, const gpt_attn_layout* layout, void* workspace, size_t workspace_bytes, void* stream) {
     if (!q || !k || !v || !o || !lse || !dO || !dq || !dk || !dv) return GPT_ATTN_ERR_NULL;
     int sc = check_shape(B, H, T, D);
     if (sc != GPT_ATTN_OK) return sc;
@@ -600,11 +637,22 @@ int gpt_attn_bwd_ex(const void* q, const void* k, const void* v, const void* o, 
     Layout L;
     if ((sc = make_layout(&L, layout, H, T, D)) != GPT_ATTN_OK) return sc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if ((sc = launch_bwd_delta(o, lse, dO, B, H, T, D, workspace, m, L, st)) != GPT_ATTN_OK) return sc;
-    sc = D == 64 ? launch_bwd_grads<64>(q, k, v, dO, dk, dv, B, H, T, scale, m, L, workspace, st)
-                 : launch_bwd_grads<128>(q, k, v, dO, dk, dv, B, H, T, scale, m, L, workspace, st);
+    SinkMask sm;
+    const SinkMask* sp = sink_mask(&sm, m, sinks, H, T) ? &sm : nullptr;
+    sc = sp ? launch_bwd_delta(o, lse, dO, B, H, T, D, workspace, *sp, L, st)
+            : launch_bwd_delta(o, lse, dO, B, H, T, D, workspace, m, L, st);
+    if (sc != GPT_ATTN_OK) return sc;
+    sc = D == 64 ? launch_bwd_grads<64>(q, k, v, dO, dk, dv, B, H, T, scale, m, L, workspace, st, sp)
+                 : launch_bwd_grads<128>(q, k, v, dO, dk, dv, B, H, T, scale, m, L, workspace, st, sp);
     if (sc != GPT_ATTN_OK) return sc;
     return launch_dq_convert(dq, B, H, T, D, scale, workspace, L, st);
+}
+
+int gpt_attn_bwd_ex(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dO,
+                    void* dq, void* dk, void* dv, int B, int H, int T, int D, float scale, const gpt_attn_mask* mask,
+                    const gpt_attn_layout* layout, void* workspace, size_t workspace_bytes, void* stream) {
+    return gpt_attn_bwd_sinks(q, k, v, o, lse, dO, dq, dk, dv, B, H, T, D, scale, mask, 0, layout, workspace,
+                              workspace_bytes, stream);
 }
 
 int gpt_attn_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dO,

@@ -46,6 +46,44 @@ GPT_ATTN_HD void fwd_key_range(int qt, int window, int& lo, int& hi) {
     }
 }
 
+// Sink keys: besides its window, query i sees the first `sinks` tokens of its document (of the
+// row when it is one document), as far as they come before it.  With d the first position of
+// query i's document, key j in [d, i] is visible iff i - j < window or j - d < sinks.
+
+// First position of query i's document, clamped to [0, i].
+GPT_ATTN_HD int row_doc(int i, int doc_start_i) { return doc_start_i < 0 ? 0 : (doc_start_i > i ? i : doc_start_i); }
+
+// Key tiles one query tile visits: its sink tiles [s, s + ns), all before lo, then its window's
+// tiles [lo, hi].  ns = 0 without sinks.
+struct FwdSpan {
+    int lo, hi, s, ns;
+    GPT_ATTN_HD bool has(int j) const { return (j >= lo && j <= hi) || (j >= s && j < s + ns); }
+    GPT_ATTN_HD int count() const { return ns + hi - lo + 1; }
+    GPT_ATTN_HD int tile(int i) const { return i < ns ? s + i : lo + (i - ns); }
+};
+
+// Adds the sink tiles to query tile `sp` whose first row's document starts at `doc`.  The tile's
+// other rows belong to that document or to one that starts inside the tile, whose sinks lie in
+// tile hi, so no other tile before lo is needed.
+GPT_ATTN_HD void fwd_add_sinks(FwdSpan& sp, int doc, int sinks) {
+    sp.s = doc / kTile;
+    const int end = (int)(((long long)doc + sinks - 1) / kTile) + 1;
+    sp.ns = (end < sp.lo ? end : sp.lo) - sp.s;
+    if (sp.ns < 0) sp.ns = 0;
+}
+
+// A block of two query tiles a, b visits a's sink tiles, then [a.lo, b.hi].  For document starts
+// that increase this covers b's tiles; b is cut to it, so that any contents keep the roles of
+// the kernel in step.
+GPT_ATTN_HD void fwd_fit_pair(const FwdSpan& a, FwdSpan& b) {
+    if (b.lo < a.lo) b.lo = a.lo;
+    const int end = b.s + b.ns;
+    if (b.s != a.s && b.s < a.lo) b.s = a.lo;
+    b.ns = (end < b.lo ? end : b.lo) - b.s;
+    if (b.s == a.s && b.s + b.ns > a.s + a.ns && a.s + a.ns < a.lo) b.ns = a.ns;
+    if (b.ns < 0) b.ns = 0;
+}
+
 // Query tiles that see at least one key of key tile kt: [kt, bwd_last_query_tile(...)].
 GPT_ATTN_HD int bwd_last_query_tile(int kt, int n_tiles, int window) {
     if (window <= 0) return n_tiles - 1;
@@ -63,6 +101,30 @@ GPT_ATTN_HD int bwd_last_query_tile_lb(int kt, int n_tiles, LowerOfTile lower_of
     const int kend = kt * kTile + kTile - 1;
     int qt = kt;
     while (qt + 1 < n_tiles && lower_of_tile(qt + 1) <= kend) ++qt;
+    return qt;
+}
+
+// The same with sinks and without documents: the tiles that hold sinks are seen to the end.
+GPT_ATTN_HD int bwd_last_query_tile_sinks(int kt, int n_tiles, int window, int sinks) {
+    return kt * kTile < sinks ? n_tiles - 1 : bwd_last_query_tile(kt, n_tiles, window);
+}
+
+// The same with sinks and documents.  Query tile qt > kt sees key tile kt iff its first row's
+// window reaches it, or that row's document starts at or before the key tile's end and its sinks
+// reach past the key tile's start.  As qt grows the document starts of the first rows do not
+// decrease, so the tiles that see kt are a prefix [kt, last]: windows give a prefix, and where
+// sinks of an earlier document end before kt those of a later one that starts in kt take over
+// from kt + 1 on.
+template <typename LowerOfTile, typename DocOfTile>
+GPT_ATTN_HD int bwd_last_query_tile_sinks_lb(int kt, int n_tiles, int sinks, LowerOfTile lower_of_tile,
+                                             DocOfTile doc_of_tile) {
+    const int k0 = kt * kTile, kend = k0 + kTile - 1;
+    int qt = kt;
+    while (qt + 1 < n_tiles) {
+        const int d = doc_of_tile(qt + 1);
+        if (!(lower_of_tile(qt + 1) <= kend || (d <= kend && (long long)d + sinks > k0))) break;
+        ++qt;
+    }
     return qt;
 }
 

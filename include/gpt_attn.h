@@ -175,6 +175,32 @@ int gpt_attn_bwd_ex(const void* q, const void* k, const void* v, const void* o,
                     void* stream);
 
 /*
+ * Sliding-window attention with sinks: a model trained and served with a
+ * window keeps the first few tokens in view, so that a stream of any length
+ * has the tokens most heads put their idle weight on.  With sinks S >= 1, key
+ * j is visible to query i of head (b, h) iff, a being doc_start[b][i] (0
+ * without document starts),
+ *     a <= j <= i  and  (i - j < W_h  or  j - a < S),
+ * the W_h of `mask` as in gpt_attn_fwd_ex; a head without a window sees
+ * everything already.  sinks <= 0: none (the calls are then gpt_attn_fwd_ex
+ * and gpt_attn_bwd_ex).  sinks has no upper limit; past T it acts as T.
+ * Everything else, layouts, ownership and errors, is as for those two; o and
+ * lse of the backward pass come from gpt_attn_fwd_sinks with the same mask and
+ * sinks, and its workspace has gpt_attn_bwd_sinks_workspace_bytes bytes
+ * (window: the largest of the call's windows; 0 for shapes the pass rejects).
+ * The form for new tokens against a cache is gpt_attn_paged_decode.
+ */
+int gpt_attn_fwd_sinks(const void* q, const void* k, const void* v, void* o, float* lse,
+                       int B, int H, int T, int D, float scale, const gpt_attn_mask* mask,
+                       int sinks, const gpt_attn_layout* layout, void* stream);
+size_t gpt_attn_bwd_sinks_workspace_bytes(int B, int H, int T, int D, int window, int sinks);
+int gpt_attn_bwd_sinks(const void* q, const void* k, const void* v, const void* o,
+                       const float* lse, const void* dO, void* dq, void* dk, void* dv,
+                       int B, int H, int T, int D, float scale, const gpt_attn_mask* mask,
+                       int sinks, const gpt_attn_layout* layout, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/*
  * The three stages gpt_attn_bwd runs, in this order, exposed so callers can
  * schedule or time them separately.  Same arguments, layouts, ownership and
  * error codes as gpt_attn_bwd; the workspace must be the same buffer for all
