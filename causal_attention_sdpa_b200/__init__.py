@@ -11,6 +11,8 @@ Entry points (same names as the C ABI, see include/gpt_attn.h):
                workspace=None, stream=None) -> (dq, dk, dv)
   gpt_attn_bwd_workspace_bytes(B, H, T, D) -> int
   gpt_attn_fwd_sinks / gpt_attn_bwd_sinks: a sliding window with first tokens that stay visible
+  gpt_attn_paged_append / _decode / _accept: new or drafted tokens over a paged key/value cache
+  gpt_attn_pages_reserve / _fork / _free / _compact / _copy: the pages themselves
   gpt_attn_check(stream=None) -> int
   gpt_attn_status_string(status) -> str
 Tensors are bf16 contiguous [B, H, T, D] on the GPU; lse is fp32 [B, H, T].
@@ -40,7 +42,10 @@ EXPORTED = ("gpt_attn_fwd", "gpt_attn_bwd", "gpt_attn_bwd_workspace_bytes", "gpt
             "gpt_attn_debug_wait_timeout", "gpt_attn_bwd_noalloc", "gpt_attn_tmap_cache_stats",
             "gpt_attn_fwd_ex", "gpt_attn_bwd_ex", "gpt_attn_decode", "gpt_attn_decode_workspace_bytes",
             "gpt_attn_debug_skip_load", "gpt_attn_qk_prologue_fwd", "gpt_attn_qk_prologue_bwd",
-            "gpt_attn_fwd_sinks", "gpt_attn_bwd_sinks", "gpt_attn_bwd_sinks_workspace_bytes")
+            "gpt_attn_fwd_sinks", "gpt_attn_bwd_sinks", "gpt_attn_bwd_sinks_workspace_bytes",
+            "gpt_attn_paged_append", "gpt_attn_paged_decode", "gpt_attn_paged_decode_workspace_bytes",
+            "gpt_attn_paged_accept", "gpt_attn_pages_reserve", "gpt_attn_pages_fork", "gpt_attn_pages_free",
+            "gpt_attn_pages_compact", "gpt_attn_pages_copy", "gpt_attn_pages_workspace_bytes")
 
 
 class GptAttnStrides(ctypes.Structure):
@@ -58,6 +63,14 @@ class GptAttnMask(ctypes.Structure):
     optional document starts (device int32 [B, T])."""
     _fields_ = [("window", ctypes.c_int), ("head_windows", ctypes.POINTER(ctypes.c_int)),
                 ("doc_start", ctypes.c_void_p)]
+
+
+class GptAttnPagedCache(ctypes.Structure):
+    """The C ABI's gpt_attn_paged_cache: pools, table and lengths of a paged key/value cache."""
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("lens", ctypes.c_void_p)] + [(n, ctypes.c_int) for n in ("B", "Hkv", "D", "n_pages", "page",
+                                                                         "max_pages")]
+
 
 _lib = None
 
@@ -119,6 +132,27 @@ def lib() -> ctypes.CDLL:
         L.gpt_attn_qk_prologue_fwd.restype = i
         L.gpt_attn_qk_prologue_bwd.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, i, f, spp, vp]
         L.gpt_attn_qk_prologue_bwd.restype = i
+        cp = ctypes.POINTER(GptAttnPagedCache)
+        L.gpt_attn_paged_append.argtypes = [cp, vp, vp, i, vp, spp, vp]
+        L.gpt_attn_paged_append.restype = i
+        L.gpt_attn_paged_decode_workspace_bytes.argtypes = [i, i, i, i, i]
+        L.gpt_attn_paged_decode_workspace_bytes.restype = sz
+        L.gpt_attn_paged_decode.argtypes = [vp, cp, vp, vp, vp, vp, i, i, f, i, i, spp, vp, sz, vp]
+        L.gpt_attn_paged_decode.restype = i
+        L.gpt_attn_paged_accept.argtypes = [cp, vp, vp, i, vp]
+        L.gpt_attn_paged_accept.restype = i
+        L.gpt_attn_pages_workspace_bytes.argtypes = [i, i, i]
+        L.gpt_attn_pages_workspace_bytes.restype = sz
+        L.gpt_attn_pages_reserve.argtypes = [vp, vp, vp, i, i, i, i, vp, vp, vp, sz, vp]
+        L.gpt_attn_pages_reserve.restype = i
+        L.gpt_attn_pages_fork.argtypes = [vp, vp, vp, i, i, i, i, vp, vp, vp, vp, sz, vp]
+        L.gpt_attn_pages_fork.restype = i
+        L.gpt_attn_pages_free.argtypes = [vp, vp, vp, i, i, i, vp, vp]
+        L.gpt_attn_pages_free.restype = i
+        L.gpt_attn_pages_compact.argtypes = [vp, vp, i, i, i, vp, vp, vp, vp, vp, sz, vp]
+        L.gpt_attn_pages_compact.restype = i
+        L.gpt_attn_pages_copy.argtypes = [vp, vp, i, i, i, i, vp, i, vp, vp]
+        L.gpt_attn_pages_copy.restype = i
         L.gpt_attn_debug_skip_load.argtypes = [i]
         L.gpt_attn_debug_skip_load.restype = i
         L.gpt_attn_debug_wait_timeout.argtypes = [i, vp]
@@ -487,6 +521,212 @@ def gpt_attn_decode(q, k_cache, v_cache, seq_lens, scale=None, window=0, o=None,
     if rc != GPT_ATTN_OK:
         raise GptAttnError(rc, "gpt_attn_decode")
     return o, lse
+
+
+def _check_int32(name, t, shape, device):
+    import torch
+    if t.dtype != torch.int32 or t.device != device or not t.is_cuda or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)} on {device}")
+
+
+def _check_pools(k_pages, v_pages):
+    import torch
+    if k_pages.dim() != 4 or not k_pages.is_cuda:
+        raise ValueError("k_pages must be a contiguous CUDA bf16 tensor [n_pages, Hkv, page, D]")
+    for n, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        if t.dtype != torch.bfloat16 or t.device != k_pages.device or t.shape != k_pages.shape or \
+                not t.is_contiguous():
+            raise ValueError(f"{n} must be a contiguous bf16 tensor of shape {tuple(k_pages.shape)} on "
+                             f"{k_pages.device}")
+
+
+def _paged_cache(k_pages, v_pages, table, lens):
+    """A GptAttnPagedCache of the checked tensors."""
+    _check_pools(k_pages, v_pages)
+    if table.dim() != 2:
+        raise ValueError("table must be a contiguous int32 tensor [B, max_pages]")
+    _check_int32("table", table, table.shape, k_pages.device)
+    B, M = table.shape
+    _check_int32("lens", lens, (B,), k_pages.device)
+    P, Hkv, page, D = k_pages.shape
+    return GptAttnPagedCache(k_pages.data_ptr(), v_pages.data_ptr(), table.data_ptr(), lens.data_ptr(), B, Hkv, D, P,
+                             page, M)
+
+
+def _pair_strides(a, b):
+    """Strides of two [b, h, n, d] tensors, or None when both are contiguous; a dimension of size 1
+    is never stepped along, so its stride does not matter."""
+    if a.is_contiguous() and b.is_contiguous():
+        return None
+    return (GptAttnStrides * 2)(*[GptAttnStrides(*[t.stride(i) if t.shape[i] > 1 else 0 for i in range(3)])
+                                  for t in (a, b)])
+
+
+def gpt_attn_paged_append(k_pages, v_pages, table, lens, k_new, v_new, n_new=None, stream=None):
+    """Writes the rows of N new tokens (k_new, v_new: bf16 [B, Hkv, N, D] views) of every sequence into
+    its pages, token n at position lens[b] + n; n_new (int32 [B]): how many of them are used."""
+    cache = _paged_cache(k_pages, v_pages, table, lens)
+    N = k_new.shape[2] if k_new.dim() == 4 else 0
+    for n, t in (("k_new", k_new), ("v_new", v_new)):
+        _check_view(n, t, (cache.B, cache.Hkv, N, cache.D))
+        if t.device != k_pages.device:
+            raise ValueError(f"{n} must be on {k_pages.device}")
+    if n_new is not None:
+        _check_int32("n_new", n_new, (cache.B,), k_pages.device)
+    _launch("gpt_attn_paged_append", k_pages.device, stream, ctypes.byref(cache), _ptr(k_new), _ptr(v_new), N,
+            _ptr(n_new), _pair_strides(k_new, v_new))
+
+
+def gpt_attn_paged_decode_workspace_bytes(B, H, Hkv, N, D) -> int:
+    return int(lib().gpt_attn_paged_decode_workspace_bytes(int(B), int(H), int(Hkv), int(N), int(D)))
+
+
+def gpt_attn_paged_decode(q, k_pages, v_pages, table, lens, parents=None, n_new=None, scale=None, window=0, sinks=0,
+                          o=None, lse=None, workspace=None, stream=None):
+    """Attention of N new tokens of every sequence (q: bf16 [B, H, N, D] view; their keys and values
+    already appended) over the paged cache and, by the tree `parents` (int32 [B, N]; None: one after the
+    other), over each other.  With a window each sees the tokens within it and the first `sinks` ones.
+    Returns (o [B, H, N, D], lse [B, H, N])."""
+    import torch
+    cache = _paged_cache(k_pages, v_pages, table, lens)
+    if q.dim() != 4:
+        raise ValueError("q must be a CUDA bf16 [B, H, N, D] view")
+    B, H, N, D = q.shape
+    device = k_pages.device
+    _check_view("q", q, (cache.B, H, N, cache.D))
+    if o is None:
+        o = torch.empty((B, H, N, D), dtype=q.dtype, device=device)
+    else:
+        _check_view("o", o, q.shape)
+    if q.device != device or o.device != device:
+        raise ValueError(f"q and o must be on {device}")
+    if lse is None:
+        lse = torch.empty((B, H, N), dtype=torch.float32, device=device)
+    else:
+        _check_tensor("lse", lse, torch.float32, (B, H, N), device)
+    if parents is not None:
+        _check_int32("parents", parents, (B, N), device)
+    if n_new is not None:
+        _check_int32("n_new", n_new, (B,), device)
+    if workspace is None:
+        need = gpt_attn_paged_decode_workspace_bytes(B, H, cache.Hkv, N, D)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    else:
+        _check_workspace(workspace, device)
+    scale = 1.0 / math.sqrt(D) if scale is None else scale
+    _launch("gpt_attn_paged_decode", device, stream, _ptr(q), ctypes.byref(cache), _ptr(n_new), _ptr(parents), _ptr(o),
+            _ptr(lse), H, N, float(scale), int(window), int(sinks), _pair_strides(q, o), _ptr(workspace),
+            workspace.numel() * workspace.element_size())
+    return o, lse
+
+
+def gpt_attn_paged_accept(k_pages, v_pages, table, lens, accepted, n_accepted, stream=None):
+    """Moves the rows of the accepted nodes up: node accepted[b, i] (int32 [B, N]) to position
+    lens[b] + i for i < n_accepted[b] (int32 [B]).  lens itself is the caller's to change."""
+    cache = _paged_cache(k_pages, v_pages, table, lens)
+    if accepted.dim() != 2:
+        raise ValueError("accepted must be a contiguous int32 tensor [B, N]")
+    _check_int32("accepted", accepted, (cache.B, accepted.shape[1]), k_pages.device)
+    _check_int32("n_accepted", n_accepted, (cache.B,), k_pages.device)
+    _launch("gpt_attn_paged_accept", k_pages.device, stream, ctypes.byref(cache), _ptr(accepted), _ptr(n_accepted),
+            accepted.shape[1])
+
+
+def gpt_attn_pages_workspace_bytes(S, M, P) -> int:
+    return int(lib().gpt_attn_pages_workspace_bytes(int(S), int(M), int(P)))
+
+
+def _check_state(table, refs, lens=None):
+    """Table, lengths and holders of the pages; returns (S, M, P, device)."""
+    if table.dim() != 2 or refs.dim() != 1:
+        raise ValueError("table must be an int32 tensor [S, M] and refs one [P]")
+    _check_int32("table", table, table.shape, table.device)
+    _check_int32("refs", refs, refs.shape, table.device)
+    if lens is not None:
+        _check_int32("lens", lens, table.shape[:1], table.device)
+    return (*table.shape, refs.shape[0], table.device)
+
+
+def _pages_workspace(workspace, S, M, P, device):
+    import torch
+    if workspace is None:
+        return torch.empty(max(gpt_attn_pages_workspace_bytes(S, M, P), 16), dtype=torch.uint8, device=device)
+    _check_workspace(workspace, device)
+    return workspace
+
+
+def gpt_attn_pages_reserve(table, lens, refs, page, tokens, status=None, workspace=None, stream=None):
+    """Gives every slot pages for tokens[s] (int32 [S]) more tokens, the lowest free ones first; table
+    and refs change in place.  Returns status int32 [S]: 0 nothing asked, 1 done, -1 refused (the table's
+    row is too short), -2 not enough free pages."""
+    import torch
+    S, M, P, device = _check_state(table, refs, lens)
+    _check_int32("tokens", tokens, (S,), device)
+    if status is None:
+        status = torch.empty(S, dtype=torch.int32, device=device)
+    else:
+        _check_int32("status", status, (S,), device)
+    ws = _pages_workspace(workspace, S, M, P, device)
+    _launch("gpt_attn_pages_reserve", device, stream, _ptr(table), _ptr(lens), _ptr(refs), S, M, P, int(page),
+            _ptr(tokens), _ptr(status), _ptr(ws), ws.numel() * ws.element_size())
+    return status
+
+
+def gpt_attn_pages_fork(table, lens, refs, page, parents, status=None, pairs=None, workspace=None, stream=None):
+    """Slot s becomes a copy of slot parents[s] (int32 [S], negative: nothing asked): full pages are
+    shared, a partial last page gets a page of its own.  Table, lens and refs change in place.  Returns
+    (status int32 [S], pairs int32 [S, 2]): status as for gpt_attn_pages_reserve, pairs the pages to copy
+    with gpt_attn_pages_copy in every layer's pools."""
+    import torch
+    S, M, P, device = _check_state(table, refs, lens)
+    _check_int32("parents", parents, (S,), device)
+    if status is None:
+        status = torch.empty(S, dtype=torch.int32, device=device)
+    else:
+        _check_int32("status", status, (S,), device)
+    if pairs is None:
+        pairs = torch.empty((S, 2), dtype=torch.int32, device=device)
+    else:
+        _check_int32("pairs", pairs, (S, 2), device)
+    ws = _pages_workspace(workspace, S, M, P, device)
+    _launch("gpt_attn_pages_fork", device, stream, _ptr(table), _ptr(lens), _ptr(refs), S, M, P, int(page),
+            _ptr(parents), _ptr(status), _ptr(pairs), _ptr(ws), ws.numel() * ws.element_size())
+    return status, pairs
+
+
+def gpt_attn_pages_free(table, lens, refs, drop, stream=None):
+    """Slots with drop[s] > 0 (int32 [S]) give their pages back; table, lens and refs change in place."""
+    S, M, P, device = _check_state(table, refs, lens)
+    _check_int32("drop", drop, (S,), device)
+    _launch("gpt_attn_pages_free", device, stream, _ptr(table), _ptr(lens), _ptr(refs), S, M, P, _ptr(drop))
+
+
+def gpt_attn_pages_compact(table, refs, workspace=None, stream=None):
+    """Packs the n pages in use into places 0 to n - 1.  Returns (new_table, new_refs, pairs int32
+    [P // 2, 2], moves int32 [1]); gpt_attn_pages_copy(k, v, pairs, n_pairs=moves) moves the pages."""
+    import torch
+    S, M, P, device = _check_state(table, refs)
+    new_table, new_refs = torch.empty_like(table), torch.empty_like(refs)
+    pairs = torch.empty((P // 2, 2), dtype=torch.int32, device=device)
+    moves = torch.empty(1, dtype=torch.int32, device=device)
+    ws = _pages_workspace(workspace, S, M, P, device)
+    _launch("gpt_attn_pages_compact", device, stream, _ptr(table), _ptr(refs), S, M, P, _ptr(new_table),
+            _ptr(new_refs), _ptr(pairs), _ptr(moves), _ptr(ws), ws.numel() * ws.element_size())
+    return new_table, new_refs, pairs, moves
+
+
+def gpt_attn_pages_copy(k_pages, v_pages, pairs, n_pairs=None, stream=None):
+    """Copies page pairs[i, 0] onto page pairs[i, 1] in both pools, for the first n_pairs (int32 [1] on
+    the device; None: all) rows of pairs (int32 [n, 2]); rows with a page outside the pools are skipped."""
+    _check_pools(k_pages, v_pages)
+    if pairs.dim() != 2:
+        raise ValueError("pairs must be a contiguous int32 tensor [n, 2]")
+    _check_int32("pairs", pairs, (pairs.shape[0], 2), k_pages.device)
+    if n_pairs is not None:
+        _check_int32("n_pairs", n_pairs, (1,), k_pages.device)
+    P, Hkv, page, D = k_pages.shape
+    _launch("gpt_attn_pages_copy", k_pages.device, stream, _ptr(k_pages), _ptr(v_pages), P, Hkv, page, D, _ptr(pairs),
+            pairs.shape[0], _ptr(n_pairs))
 
 
 def gpt_attn_qk_prologue_fwd(q_raw, k_raw, qk_norm=True, rope_base=10000.0, q_out=None, k_out=None, stream=None):

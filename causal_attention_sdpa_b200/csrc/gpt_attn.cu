@@ -16,10 +16,13 @@
 #include "attn_decode.cuh"
 #include "attn_fwd.cuh"
 #include "gpt_attn.h"
+#include "paged_decode.cuh"
+#include "pages.cuh"
 #include "qk_prologue.cuh"
 #include "tmap_cache.h"
 
 extern "C" size_t gpt_attn_bwd_workspace_bytes(int B, int H, int T, int D);
+extern "C" size_t gpt_attn_pages_workspace_bytes(int S, int M, int P);
 
 namespace gpt_attn {
 namespace {
@@ -499,6 +502,103 @@ int launch_prologue(bool backward, const PrologueParams& p, int D, cudaStream_t 
     return cudaGetLastError() == cudaSuccess ? GPT_ATTN_OK : GPT_ATTN_ERR_CUDA;
 }
 
+// A paged cache description, checked: sizes, alignment, and that row numbers fit an int.
+int check_cache(PagedPools* c, const gpt_attn_paged_cache* a) {
+    if (!a || !a->k_pages || !a->v_pages || !a->table || !a->lens) return GPT_ATTN_ERR_NULL;
+    if (a->B < 1 || a->Hkv < 1 || a->n_pages < 1 || a->page < 1 || a->max_pages < 1) return GPT_ATTN_ERR_SHAPE;
+    if (a->D != 64 && a->D != 128) return GPT_ATTN_ERR_UNSUPPORTED_D;
+    if ((long long)a->max_pages * a->page > (1LL << 30)) return GPT_ATTN_ERR_SHAPE;
+    const long long heads = (long long)a->n_pages * a->Hkv;
+    if (heads > 0x7fffffffLL || heads * a->page > 0x7fffffffLL) return GPT_ATTN_ERR_SHAPE;
+    if ((long long)a->B * a->Hkv > 0x7fffffffLL) return GPT_ATTN_ERR_SHAPE;       // grid x
+    if (misaligned(a->k_pages) || misaligned(a->v_pages) || (reinterpret_cast<uintptr_t>(a->table) & 3u) ||
+        (reinterpret_cast<uintptr_t>(a->lens) & 3u))
+        return GPT_ATTN_ERR_ALIGN;
+    c->k = static_cast<__nv_bfloat16*>(a->k_pages);
+    c->v = static_cast<__nv_bfloat16*>(a->v_pages);
+    c->table = a->table;
+    c->lens = a->lens;
+    c->n_pages = a->n_pages;
+    c->Hkv = a->Hkv;
+    c->page = a->page;
+    c->max_pages = a->max_pages;
+    c->cap = a->max_pages * a->page;
+    return GPT_ATTN_OK;
+}
+
+bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+
+// Row blocks of an item and 16-row tiles of a block of the paged decode kernel.
+struct PagedShape {
+    int R, RB, MT;
+};
+PagedShape paged_shape(int H, int Hkv, int N) {
+    PagedShape s;
+    s.R = H / Hkv * N;
+    s.RB = (s.R + 63) / 64;
+    s.MT = s.R <= 16 ? 1 : (s.R <= 32 ? 2 : 4);
+    return s;
+}
+
+int check_paged_shape(int B, int H, int Hkv, int N, int D) {
+    if (B < 1 || H < 1 || Hkv < 1 || N < 1 || N > kMaxNodes || H % Hkv) return GPT_ATTN_ERR_SHAPE;
+    if (D != 64 && D != 128) return GPT_ATTN_ERR_UNSUPPORTED_D;
+    if ((long long)H / Hkv * N > (1 << 20)) return GPT_ATTN_ERR_SHAPE;
+    if ((long long)B * Hkv * paged_shape(H, Hkv, N).RB > 0x7fffffffLL) return GPT_ATTN_ERR_SHAPE;   // grid x
+    return GPT_ATTN_OK;
+}
+
+// Blocks of the paged decode kernel: all resident at once on a B200 (148 SMs); the workspace is
+// sized by them.
+constexpr int kPagedBlocks = kPagedBlocksPerSm * 148;
+
+template <int D, int MT>
+int launch_paged(const PagedParams& p, int grid, cudaStream_t st) {
+    const size_t smem = sizeof(PagedSmem<D>) + 1024;
+    if (!set_smem(paged_decode_kernel<D, MT>, smem)) return GPT_ATTN_ERR_CUDA;
+    paged_decode_kernel<D, MT><<<grid, kPagedThreads, smem, st>>>(p);
+    constexpr int kRowsAtOnce = kPagedThreads / (D / 4);
+    const int rows = p.R < 16 * MT ? p.R : 16 * MT;
+    const dim3 cgrid((unsigned)(p.B * p.Hkv * p.RB), (unsigned)((rows + kRowsAtOnce - 1) / kRowsAtOnce));
+    paged_combine_kernel<D, MT><<<cgrid, kPagedThreads, 0, st>>>(p);
+    return cudaGetLastError() == cudaSuccess ? GPT_ATTN_OK : GPT_ATTN_ERR_CUDA;
+}
+
+template <int D>
+int launch_paged_d(const PagedParams& p, int MT, int grid, cudaStream_t st) {
+    return MT == 1 ? launch_paged<D, 1>(p, grid, st) : MT == 2 ? launch_paged<D, 2>(p, grid, st)
+                                                               : launch_paged<D, 4>(p, grid, st);
+}
+
+// Strides of n [b, h, n, d] tensors from the C ABI (nullptr: contiguous); as for layouts.
+int paged_strides(Strides* out, const gpt_attn_strides* in, const int* heads, int n, int N, int D) {
+    for (int i = 0; i < n; ++i) {
+        const int sc = prologue_strides(out + i, in ? in + i : nullptr, 1, heads[i], N, D);
+        if (sc != GPT_ATTN_OK) return sc;
+    }
+    return GPT_ATTN_OK;
+}
+
+int check_pages(int S, int M, int P) {
+    if (S < 1 || M < 1 || P < 1) return GPT_ATTN_ERR_SHAPE;
+    return (long long)S * M > 0x7fffffffLL ? GPT_ATTN_ERR_SHAPE : GPT_ATTN_OK;
+}
+
+// Workspace of the table calls: pages asked for [S] | free pages, or new places [P] | counts.
+int pages_params(PagesParams* p, int S, int M, int P, void* ws, size_t ws_bytes) {
+    const int sc = check_pages(S, M, P);
+    if (sc != GPT_ATTN_OK) return sc;
+    if (!ws || ws_bytes < gpt_attn_pages_workspace_bytes(S, M, P)) return GPT_ATTN_ERR_WORKSPACE;
+    if (misaligned(ws)) return GPT_ATTN_ERR_ALIGN;
+    p->S = S;
+    p->M = M;
+    p->P = P;
+    p->need = static_cast<int*>(ws);
+    p->list = p->need + S;
+    p->counts = p->list + P;
+    return GPT_ATTN_OK;
+}
+
 __global__ void debug_wait_kernel(uint64_t timeout_ns) {
     __shared__ uint64_t bar;
     __shared__ int abort_flag;
@@ -685,6 +785,217 @@ int gpt_attn_decode(const void* q, const void* k_cache, const void* v_cache, con
     return D == 64 ? launch_decode<64>(q, k_cache, v_cache, seq_lens, o, lse, B, H, T_max, scale, window, workspace, st)
                    : launch_decode<128>(q, k_cache, v_cache, seq_lens, o, lse, B, H, T_max, scale, window, workspace,
                                         st);
+}
+
+size_t gpt_attn_paged_decode_workspace_bytes(int B, int H, int Hkv, int N, int D) {
+    if (check_paged_shape(B, H, Hkv, N, D) != GPT_ATTN_OK) return 0;
+    const size_t rows = (size_t)16 * paged_shape(H, Hkv, N).MT;
+    return 2 * (size_t)kPagedBlocks * rows * (D + 2) * sizeof(float) + ((size_t)B + 2) * sizeof(long long);
+}
+
+int gpt_attn_paged_decode(const void* q, const gpt_attn_paged_cache* cache, const int* n_new, const int* parents,
+                          void* o, float* lse, int H, int N, float scale, int window, int sinks,
+                          const gpt_attn_strides* strides, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!q || !o || !lse) return GPT_ATTN_ERR_NULL;
+    PagedPools c;
+    int sc = check_cache(&c, cache);
+    if (sc != GPT_ATTN_OK) return sc;
+    const int B = cache->B, D = cache->D;
+    if ((sc = check_paged_shape(B, H, c.Hkv, N, D)) != GPT_ATTN_OK) return sc;
+    if (!workspace || workspace_bytes < gpt_attn_paged_decode_workspace_bytes(B, H, c.Hkv, N, D))
+        return GPT_ATTN_ERR_WORKSPACE;
+    if (misaligned(q) || misaligned(o) || misaligned(workspace) || misaligned4(lse) || misaligned4(n_new) ||
+        misaligned4(parents))
+        return GPT_ATTN_ERR_ALIGN;
+    PagedParams p;
+    Strides st[2];
+    const int heads[2] = {H, H};
+    if ((sc = paged_strides(st, strides, heads, 2, N, D)) != GPT_ATTN_OK) return sc;
+    const PagedShape s = paged_shape(H, c.Hkv, N);
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.k = c.k;
+    p.v = c.v;
+    p.table = c.table;
+    p.lens = c.lens;
+    p.n_new = n_new;
+    p.parents = parents;
+    p.o = static_cast<__nv_bfloat16*>(o);
+    p.lse = lse;
+    p.q_str = st[0];
+    p.o_str = st[1];
+    p.part_o = static_cast<float*>(workspace);
+    p.part_ml = p.part_o + 2 * (size_t)kPagedBlocks * 16 * s.MT * D;
+    p.prefix = reinterpret_cast<long long*>(p.part_ml + 2 * (size_t)kPagedBlocks * 16 * s.MT * 2);
+    p.B = B;
+    p.H = H;
+    p.Hkv = c.Hkv;
+    p.G = H / c.Hkv;
+    p.N = N;
+    p.R = s.R;
+    p.RB = s.RB;
+    p.page = c.page;
+    p.max_pages = c.max_pages;
+    p.n_pages = c.n_pages;
+    p.cap = c.cap;
+    p.window = window > 0 ? window : 0;
+    p.sinks = sinks > 0 && window > 0 ? sinks : 0;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    // No more blocks than the tables can name tiles.
+    const long long most = (long long)B * c.Hkv * s.RB * ((c.cap + kPagedTile - 1) / kPagedTile);
+    const int grid = (int)(most < kPagedBlocks ? most : kPagedBlocks);
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    return D == 64 ? launch_paged_d<64>(p, s.MT, grid, cs) : launch_paged_d<128>(p, s.MT, grid, cs);
+}
+
+int gpt_attn_paged_append(const gpt_attn_paged_cache* cache, const void* k_new, const void* v_new, int N,
+                          const int* n_new, const gpt_attn_strides* strides, void* stream) {
+    if (!k_new || !v_new) return GPT_ATTN_ERR_NULL;
+    AppendParams p;
+    int sc = check_cache(&p.c, cache);
+    if (sc != GPT_ATTN_OK) return sc;
+    if (N < 1) return GPT_ATTN_ERR_SHAPE;
+    if (misaligned(k_new) || misaligned(v_new) || misaligned4(n_new)) return GPT_ATTN_ERR_ALIGN;
+    Strides st[2];
+    const int heads[2] = {cache->Hkv, cache->Hkv};
+    if ((sc = paged_strides(st, strides, heads, 2, N, cache->D)) != GPT_ATTN_OK) return sc;
+    p.k_new = static_cast<const __nv_bfloat16*>(k_new);
+    p.v_new = static_cast<const __nv_bfloat16*>(v_new);
+    p.k_str = st[0];
+    p.v_str = st[1];
+    p.n_new = n_new;
+    p.N = N;
+    const long long rows = (long long)cache->B * cache->Hkv;
+    if (N > (0x7fffffffLL * 256 / 16) / rows) return GPT_ATTN_ERR_SHAPE;            // grid size
+    p.chunks = rows * N * (cache->D / 8);
+    const unsigned grid = (unsigned)((p.chunks + 255) / 256);
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    if (cache->D == 64) paged_append_kernel<64><<<grid, 256, 0, cs>>>(p);
+    else paged_append_kernel<128><<<grid, 256, 0, cs>>>(p);
+    return cudaGetLastError() == cudaSuccess ? GPT_ATTN_OK : GPT_ATTN_ERR_CUDA;
+}
+
+int gpt_attn_paged_accept(const gpt_attn_paged_cache* cache, const int* accepted, const int* n_accepted, int N,
+                          void* stream) {
+    if (!accepted || !n_accepted) return GPT_ATTN_ERR_NULL;
+    AcceptParams p;
+    const int sc = check_cache(&p.c, cache);
+    if (sc != GPT_ATTN_OK) return sc;
+    if (N < 1 || N > kMaxNodes) return GPT_ATTN_ERR_SHAPE;
+    if (misaligned4(accepted) || misaligned4(n_accepted)) return GPT_ATTN_ERR_ALIGN;
+    p.accepted = accepted;
+    p.n_accepted = n_accepted;
+    p.N = N;
+    const unsigned grid = (unsigned)(cache->B * cache->Hkv);
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    if (cache->D == 64) paged_accept_kernel<64><<<grid, kAcceptThreads, 0, cs>>>(p);
+    else paged_accept_kernel<128><<<grid, kAcceptThreads, 0, cs>>>(p);
+    return cudaGetLastError() == cudaSuccess ? GPT_ATTN_OK : GPT_ATTN_ERR_CUDA;
+}
+
+size_t gpt_attn_pages_workspace_bytes(int S, int M, int P) {
+    if (check_pages(S, M, P) != GPT_ATTN_OK) return 0;
+    return ((size_t)S + P + 4 * kPagesCluster) * sizeof(int);
+}
+
+int gpt_attn_pages_reserve(int* table, const int* lens, int* refs, int S, int M, int P, int page, const int* tokens,
+                           int* status, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!table || !lens || !refs || !tokens || !status) return GPT_ATTN_ERR_NULL;
+    PagesParams p{};
+    const int sc = pages_params(&p, S, M, P, workspace, workspace_bytes);
+    if (sc != GPT_ATTN_OK) return sc;
+    if (page < 1) return GPT_ATTN_ERR_SHAPE;
+    if (misaligned4(table) || misaligned4(lens) || misaligned4(refs) || misaligned4(tokens) || misaligned4(status))
+        return GPT_ATTN_ERR_ALIGN;
+    p.table = table;
+    p.lens = const_cast<int*>(lens);
+    p.refs = refs;
+    p.page = page;
+    p.arg = tokens;
+    p.status = status;
+    pages_take_kernel<false><<<kPagesCluster, kPagesThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    return cudaGetLastError() == cudaSuccess ? GPT_ATTN_OK : GPT_ATTN_ERR_CUDA;
+}
+
+int gpt_attn_pages_fork(int* table, int* lens, int* refs, int S, int M, int P, int page, const int* parents,
+                        int* status, int* pairs, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!table || !lens || !refs || !parents || !status || !pairs) return GPT_ATTN_ERR_NULL;
+    PagesParams p{};
+    const int sc = pages_params(&p, S, M, P, workspace, workspace_bytes);
+    if (sc != GPT_ATTN_OK) return sc;
+    if (page < 1) return GPT_ATTN_ERR_SHAPE;
+    if (misaligned4(table) || misaligned4(lens) || misaligned4(refs) || misaligned4(parents) || misaligned4(status) ||
+        (reinterpret_cast<uintptr_t>(pairs) & 7u))
+        return GPT_ATTN_ERR_ALIGN;
+    p.table = table;
+    p.lens = lens;
+    p.refs = refs;
+    p.page = page;
+    p.arg = parents;
+    p.status = status;
+    p.pairs = reinterpret_cast<int2*>(pairs);
+    pages_take_kernel<true><<<kPagesCluster, kPagesThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    return cudaGetLastError() == cudaSuccess ? GPT_ATTN_OK : GPT_ATTN_ERR_CUDA;
+}
+
+int gpt_attn_pages_free(int* table, int* lens, int* refs, int S, int M, int P, const int* drop, void* stream) {
+    if (!table || !lens || !refs || !drop) return GPT_ATTN_ERR_NULL;
+    const int sc = check_pages(S, M, P);
+    if (sc != GPT_ATTN_OK) return sc;
+    if (misaligned4(table) || misaligned4(lens) || misaligned4(refs) || misaligned4(drop)) return GPT_ATTN_ERR_ALIGN;
+    PagesParams p{};
+    p.table = table;
+    p.lens = lens;
+    p.refs = refs;
+    p.S = S;
+    p.M = M;
+    p.P = P;
+    p.arg = drop;
+    pages_free_kernel<<<(unsigned)((S + 7LL) / 8), 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    return cudaGetLastError() == cudaSuccess ? GPT_ATTN_OK : GPT_ATTN_ERR_CUDA;
+}
+
+int gpt_attn_pages_compact(const int* table, const int* refs, int S, int M, int P, int* new_table, int* new_refs,
+                           int* pairs, int* moves, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!table || !refs || !new_table || !new_refs || (!pairs && P > 1) || !moves) return GPT_ATTN_ERR_NULL;
+    PagesParams p{};
+    const int sc = pages_params(&p, S, M, P, workspace, workspace_bytes);
+    if (sc != GPT_ATTN_OK) return sc;
+    if (misaligned4(table) || misaligned4(refs) || misaligned4(new_table) || misaligned4(new_refs) ||
+        misaligned4(moves) || (reinterpret_cast<uintptr_t>(pairs) & 7u))
+        return GPT_ATTN_ERR_ALIGN;
+    p.table = const_cast<int*>(table);
+    p.refs = const_cast<int*>(refs);
+    p.new_table = new_table;
+    p.new_refs = new_refs;
+    p.pairs = reinterpret_cast<int2*>(pairs);
+    p.moves = moves;
+    pages_compact_kernel<<<kPagesCluster, kPagesThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    return cudaGetLastError() == cudaSuccess ? GPT_ATTN_OK : GPT_ATTN_ERR_CUDA;
+}
+
+int gpt_attn_pages_copy(void* k_pages, void* v_pages, int n_pages, int Hkv, int page, int D, const int* pairs,
+                        int n_max, const int* n_pairs, void* stream) {
+    if (!k_pages || !v_pages || (!pairs && n_max > 0)) return GPT_ATTN_ERR_NULL;
+    if (n_pages < 1 || Hkv < 1 || page < 1 || n_max < 0) return GPT_ATTN_ERR_SHAPE;
+    if (D != 64 && D != 128) return GPT_ATTN_ERR_UNSUPPORTED_D;
+    if ((long long)Hkv * page > 0x7fffffffLL / (D / 8) - kCopyUnit) return GPT_ATTN_ERR_SHAPE;
+    if (misaligned(k_pages) || misaligned(v_pages) || (reinterpret_cast<uintptr_t>(pairs) & 7u) ||
+        misaligned4(n_pairs))
+        return GPT_ATTN_ERR_ALIGN;
+    if (n_max == 0) return GPT_ATTN_OK;
+    CopyParams p;
+    p.k = static_cast<uint4*>(k_pages);
+    p.v = static_cast<uint4*>(v_pages);
+    p.pairs = reinterpret_cast<const int2*>(pairs);
+    p.n_pairs = n_pairs;
+    p.max_pairs = n_max;
+    p.n_pages = n_pages;
+    p.page_chunks = Hkv * page * (D / 8);
+    p.units = (p.page_chunks + kCopyUnit - 1) / kCopyUnit;
+    const long long most = 2LL * n_max * p.units, resident = 8LL * sm_count();
+    pages_copy_kernel<<<(unsigned)(most < resident ? most : resident), kCopyThreads, 0,
+                        static_cast<cudaStream_t>(stream)>>>(p);
+    return cudaGetLastError() == cudaSuccess ? GPT_ATTN_OK : GPT_ATTN_ERR_CUDA;
 }
 
 int gpt_attn_qk_prologue_fwd(const void* q_raw, const void* k_raw, void* q_out, void* k_out, int B, int H, int T,

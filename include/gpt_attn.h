@@ -278,6 +278,137 @@ int gpt_attn_decode(const void* q, const void* k_cache, const void* v_cache, con
                     void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Paged key/value cache, for serving many sequences from one pool of memory.
+ * Keys and values of one layer live in two pools of pages of `page` tokens;
+ * the table gives each slot's pages in the order of its tokens, so position x
+ * of slot b is row x % page of page table[b][x / page], and layers share one
+ * table.  All pointers are device memory; lengths and tables are read on the
+ * device, so every call can be captured once and replayed as sequences grow.
+ *   k_pages,
+ *   v_pages   : bf16 [n_pages, Hkv, page, D] contiguous, 16-byte aligned.
+ *   table     : const int32 [B, max_pages]; an entry outside [0, n_pages) is a
+ *               missing page: its tokens are not seen and nothing is written
+ *               to them.
+ *   lens      : const int32 [B] cached tokens (clamped to [0, max_pages *
+ *               page]).  The new tokens of a call stand behind them; no call
+ *               on the pools changes lens, the caller adds what it keeps.
+ * D is 64 or 128; page any size from 1; max_pages * page <= 2^30 and n_pages *
+ * Hkv * page < 2^31.
+ */
+typedef struct gpt_attn_paged_cache {
+    void* k_pages;
+    void* v_pages;
+    const int* table;
+    const int* lens;
+    int B, Hkv, D;
+    int n_pages, page, max_pages;
+} gpt_attn_paged_cache;
+
+/*
+ * Writes the keys and values of N new tokens of every sequence into its pages:
+ * token n of sequence b to position lens[b] + n.
+ *   k_new, v_new : const bf16 [B, Hkv, N, D]-indexed with strides[0..1] (NULL:
+ *                  contiguous; e.g. the columns of a fused projection).
+ *   n_new        : const int32 [B] on the device, or NULL for N each: new
+ *                  tokens of sequence b (clamped to [0, N]).
+ * Tokens past max_pages * page or on a missing page are dropped.  The pages
+ * written must belong to one slot each (gpt_attn_pages_fork sees to that).
+ * Errors as for gpt_attn_fwd_ex.  Asynchronous on `stream`.
+ */
+int gpt_attn_paged_append(const gpt_attn_paged_cache* cache, const void* k_new, const void* v_new,
+                          int N, const int* n_new, const gpt_attn_strides* strides, void* stream);
+
+/*
+ * Attention of N new tokens of every sequence (1 <= N <= 64), whose keys and
+ * values are already in the pages at positions lens[b] + n (as
+ * gpt_attn_paged_append leaves them), against the cached tokens and each
+ * other.  The new tokens form a tree: parents[b][n] < n is the node that node n
+ * continues, a value that is negative (or not below n) the cached context.
+ * Node n stands at position p_n = lens[b] + depth(n), sees all cached tokens
+ * and its own ancestors, itself included, and with window >= 1 of those only
+ * the ones whose position x has p_n - x < window or x < sinks.
+ * Without parents the tokens follow one another (N = 1: plain decoding; N > 1:
+ * the last tokens of a prompt, causal).
+ *   q       : const bf16 [B, H, N, D]-indexed with strides[0], o: bf16, written,
+ *             with strides[1] (NULL: both contiguous).  H is a multiple of Hkv:
+ *             query head h reads key head h / (H / Hkv).
+ *   lse     : fp32 [B, H, N] (natural log), written.
+ *   n_new   : const int32 [B] or NULL, as above; nodes from n_new[b] on, and
+ *             nodes that see nothing, get o = 0 and lse = -inf.
+ *   parents : const int32 [B, N] or NULL.
+ *   workspace: >= gpt_attn_paged_decode_workspace_bytes(B, H, Hkv, N, D) bytes
+ *             (0 for shapes the call rejects), 16-byte aligned, contents
+ *             ignored on entry.
+ * What a node does not see does not reach it, infinities and NaN included.
+ * Memory-bound up to some hundred rows N * H / Hkv per key head.  Errors as for
+ * gpt_attn_decode.  Asynchronous on `stream`.
+ */
+size_t gpt_attn_paged_decode_workspace_bytes(int B, int H, int Hkv, int N, int D);
+int gpt_attn_paged_decode(const void* q, const gpt_attn_paged_cache* cache, const int* n_new,
+                          const int* parents, void* o, float* lse, int H, int N, float scale,
+                          int window, int sinks, const gpt_attn_strides* strides, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/*
+ * Keeps the accepted drafts: node accepted[b][i], i < n_accepted[b], moves from
+ * position lens[b] + accepted[b][i] to lens[b] + i, all rows read before one
+ * is written.  accepted: const int32 [B, N], n_accepted: const int32 [B]
+ * (clamped to [0, N]), N <= 64; nodes outside [0, N) are skipped.  The caller
+ * then adds n_accepted to lens.  Asynchronous on `stream`.
+ */
+int gpt_attn_paged_accept(const gpt_attn_paged_cache* cache, const int* accepted, const int* n_accepted,
+                          int N, void* stream);
+
+/*
+ * The pages of S slots in a pool of P pages of `page` tokens.  State, all on
+ * the device and changed in place: table int32 [S, M] (a slot's pages in order,
+ * then -1), lens int32 [S], refs int32 [P] (slots that hold each page; 0:
+ * free).  Results do not depend on the order of threads: the lowest free pages
+ * go to the lowest slots.  status int32 [S] is written for every slot: 0
+ * nothing asked, 1 done, -1 refused, -2 not enough free pages; a slot with a
+ * negative status is left as it was.  S, M, P >= 1 and S * M < 2^31.
+ * Asynchronous on `stream`; the workspace of reserve, fork and compact has
+ * gpt_attn_pages_workspace_bytes(S, M, P) bytes, 16-byte aligned, contents
+ * ignored on entry.
+ *
+ * gpt_attn_pages_reserve: pages for tokens[s] more tokens than lens[s] (<= 0:
+ *   nothing asked), behind those that the slot has.  -1 where M pages do not
+ *   hold them.  A slot is served if what it and all slots before it ask for
+ *   fits into the free pages.
+ * gpt_attn_pages_fork: slot s becomes a copy of slot parents[s] (negative:
+ *   nothing asked).  Full pages are shared (their refs go up); a partial last
+ *   page gets a page of its own, the copy of which the caller makes with
+ *   gpt_attn_pages_copy: pairs int32 [S, 2] receives (old, new), or (-1, -1).
+ *   Pages that the parent holds past its last token are not shared.  -1 where s
+ *   holds pages or tokens, the parent is not another slot that stays, or one of
+ *   the parent's pages is missing.  Service is in order as above.
+ * gpt_attn_pages_free: slots with drop[s] > 0 give their pages back (refs go
+ *   down, the row is filled with -1, the length becomes 0).
+ * gpt_attn_pages_compact: the new table, new refs and moves that pack the n
+ *   pages in use into places 0 to n - 1: the k-th page in use at or past place n
+ *   goes to the k-th free place before n.  table and refs are read; new_table
+ *   [S, M], new_refs [P], pairs int32 [P / 2, 2] ((from, to), then (-1, -1)) and
+ *   moves int32 [1] are written, none of them overlapping the inputs.
+ * gpt_attn_pages_copy: copies page pairs[i][0] onto page pairs[i][1] in both
+ *   pools, i < *n_pairs (device; NULL: n_max); pairs with a page outside the pool
+ *   are skipped.  No page may be copied onto twice, or be copied onto and from.
+ */
+size_t gpt_attn_pages_workspace_bytes(int S, int M, int P);
+int gpt_attn_pages_reserve(int* table, const int* lens, int* refs, int S, int M, int P, int page,
+                           const int* tokens, int* status, void* workspace, size_t workspace_bytes,
+                           void* stream);
+int gpt_attn_pages_fork(int* table, int* lens, int* refs, int S, int M, int P, int page,
+                        const int* parents, int* status, int* pairs, void* workspace,
+                        size_t workspace_bytes, void* stream);
+int gpt_attn_pages_free(int* table, int* lens, int* refs, int S, int M, int P, const int* drop,
+                        void* stream);
+int gpt_attn_pages_compact(const int* table, const int* refs, int S, int M, int P, int* new_table,
+                           int* new_refs, int* pairs, int* moves, void* workspace,
+                           size_t workspace_bytes, void* stream);
+int gpt_attn_pages_copy(void* k_pages, void* v_pages, int n_pages, int Hkv, int page, int D,
+                        const int* pairs, int n_max, const int* n_pairs, void* stream);
+
+/*
  * QK-Norm + rotary prologue of q and k (the step before attention in the
  * modded-nanogpt README's "modernised architecture" item: rotary embeddings
  * and QK-Norm; no formulas are given there, this is the reading taken).  For
