@@ -61,6 +61,7 @@ struct BwdParams {
     float scale_log2;       // scale * log2(e)
     float scale;
     uint64_t timeout_ns;
+    int n_sink_tiles;       // with sinks and without documents: key tiles of a head that hold them
 };
 
 // Last query tile that sees key tile kt of head bh (window W).
@@ -69,6 +70,13 @@ __device__ __forceinline__ int bwd_last_tile(const BwdParams& p, const Mask& mas
     if (p.last_qt) return __ldg(p.last_qt + (size_t)bh * p.n_tiles + kt);
     if constexpr (Mask::kSinks) return bwd_last_query_tile_sinks(kt, p.n_tiles, W, mask.sinks);
     return bwd_last_query_tile(kt, p.n_tiles, W);
+}
+
+// Work unit u: head and key tile.  With sinks and without documents the tiles that hold sinks go first.
+template <typename Mask>
+__device__ __forceinline__ void bwd_list_item(const BwdParams& p, int u, int& bh, int& kt) {
+    if (Mask::kSinks && p.n_sink_tiles > 0) list_item_sinks(u, p.BH, p.n_tiles, p.n_sink_tiles, p.tail, bh, kt);
+    else list_item(u, p.BH, p.n_tiles, p.tail, bh, kt);
 }
 
 // With sinks: whether key `key` of head bh is a sink, hence seen by every later query of its
@@ -237,7 +245,7 @@ attn_bwd_serial_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
     // Blocks of one head are adjacent in launch order (its Q, dO and dQ rows stay in
     // L2 across its key tiles); key tile 0 sees the most query tiles and launches first.
     int bh, kt;
-    list_item(blockIdx.x, p.BH, p.n_tiles, p.tail, bh, kt);   // unit list order of schedule.h
+    bwd_list_item<Mask>(p, blockIdx.x, bh, kt);   // unit list order of schedule.h
     const int k0 = kt * kTile;
     const int qt_lo = kt;
     const int W = mask.head_window(bh);

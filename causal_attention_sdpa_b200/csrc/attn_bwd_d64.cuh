@@ -97,7 +97,7 @@ struct Bwd64Unit {
 template <typename Mask>
 __device__ __forceinline__ Bwd64Unit bwd64_unit(int u, const BwdParams& p, const Mask& mask) {
     Bwd64Unit w;
-    list_item(u, p.BH, p.n_tiles, p.tail, w.bh, w.kt);
+    bwd_list_item<Mask>(p, u, w.bh, w.kt);
     w.W = mask.head_window(w.bh);
     w.n_q = bwd_last_tile(p, mask, w.bh, w.kt, w.W) - w.kt + 1;
     w.k0 = w.kt * kTile;

@@ -7,6 +7,7 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include <algorithm>
 #include <atomic>
 #include <mutex>
 #include <vector>
@@ -344,7 +345,9 @@ int launch_bwd_grads(const void* q, const void* k, const void* v, const void* do
     p.T_pad = w.T_pad;
     p.BH = BH;
     p.n_tiles = w.n_tiles;
-    p.tail = tail_heads(BH, p.n_tiles, sm_count());
+    p.n_sink_tiles = 0;
+    if (sinks && !mask.doc_start) p.n_sink_tiles = (int)std::min<long long>(p.n_tiles, ((long long)sinks->sinks + kTile - 1) / kTile);
+    p.tail = tail_heads(BH, std::max(1, p.n_tiles - p.n_sink_tiles), sm_count());
     p.lower2 = mask.doc_start ? w.lower2 : nullptr;
     p.last_qt = mask.doc_start ? w.last_qt : nullptr;
     p.scale_log2 = scale * 1.4426950408889634f;
@@ -557,10 +560,17 @@ int launch_paged(const PagedParams& p, int grid, cudaStream_t st) {
     const size_t smem = sizeof(PagedSmem<D>) + 1024;
     if (!set_smem(paged_decode_kernel<D, MT>, smem)) return GPT_ATTN_ERR_CUDA;
     paged_decode_kernel<D, MT><<<grid, kPagedThreads, smem, st>>>(p);
-    constexpr int kRowsAtOnce = kPagedThreads / (D / 4);
     const int rows = p.R < 16 * MT ? p.R : 16 * MT;
-    const dim3 cgrid((unsigned)(p.B * p.Hkv * p.RB), (unsigned)((rows + kRowsAtOnce - 1) / kRowsAtOnce));
-    paged_combine_kernel<D, MT><<<cgrid, kPagedThreads, 0, st>>>(p);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(p.B * p.Hkv * p.RB), (unsigned)((rows + kCombineWarps - 1) / kCombineWarps));
+    cfg.blockDim = dim3(32 * kCombineWarps);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, paged_combine_kernel<D, MT>, p) != cudaSuccess) return GPT_ATTN_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? GPT_ATTN_OK : GPT_ATTN_ERR_CUDA;
 }
 
@@ -840,6 +850,7 @@ int gpt_attn_paged_decode(const void* q, const gpt_attn_paged_cache* cache, cons
     p.window = window > 0 ? window : 0;
     p.sinks = sinks > 0 && window > 0 ? sinks : 0;
     p.scale_log2 = scale * 1.4426950408889634f;
+    p.timeout_ns = wait_timeout_ns();
     // No more blocks than the tables can name tiles.
     const long long most = (long long)B * c.Hkv * s.RB * ((c.cap + kPagedTile - 1) / kPagedTile);
     const int grid = (int)(most < kPagedBlocks ? most : kPagedBlocks);

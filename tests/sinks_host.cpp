@@ -43,4 +43,7 @@ int snk_bwd_last(const int* ds, int T, int W, int sinks, int kt) {
         kt, n_tiles, sinks, [&](int qt) { return lower_at(ds, T, W, qt * kTile); },
         [&](int qt) { return doc_at(ds, T, qt * kTile); });
 }
+void snk_list_item(int u, int BH, int n_cls, int n_s, int tail, int* bh, int* cls) {
+    list_item_sinks(u, BH, n_cls, n_s, tail, *bh, *cls);
+}
 }

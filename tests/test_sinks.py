@@ -124,6 +124,18 @@ def test_any_document_starts_keep_the_roles_in_step(S):
             assert kt <= last < -(-T // TILE)
 
 
+@pytest.mark.parametrize("BH,n,n_s", [(1, 1, 1), (24, 64, 1), (5, 7, 3), (3, 4, 4), (100, 9, 2), (2, 30, 0)])
+def test_backward_order_takes_each_unit_once_and_sink_tiles_first(S, BH, n, n_s):
+    for tail in {1, BH // 2 + 1, BH}:
+        seen = []
+        for u in range(BH * n):
+            bh, cls = ctypes.c_int(), ctypes.c_int()
+            S.snk_list_item(u, BH, n, n_s, tail, ctypes.byref(bh), ctypes.byref(cls))
+            seen.append((bh.value, cls.value))
+        assert sorted(seen) == [(b, c) for b in range(BH) for c in range(n)]
+        assert all(c < n_s for _, c in seen[:BH * n_s])
+
+
 # ------------------------------------------------------------------------------ refusals
 FAKE = 0x10000
 
