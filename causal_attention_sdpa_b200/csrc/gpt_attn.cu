@@ -3,6 +3,7 @@
 // (except in gpt_attn_check, which exists to sync).
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
 #include <stdlib.h>
 #include <string.h>
@@ -64,16 +65,17 @@ EncodeTiledFn encode_fn() {
 // layout), zero fill outside the tensor so ragged tails read as zeros.  bf16 maps are 4-D
 // (D, T, H, B) with the tensor's own token, head and batch strides, so any [b, h, t, d] view with
 // contiguous d (e.g. the q, k, v columns of a fused [B, T, 3, H, D] projection) is read and
-// written in place; the fp32 accumulator map is 3-D (D, T, B*H), contiguous.
+// written in place; the fp32 accumulator map is 3-D (D, T, B*H), contiguous; the maps of cache pools
+// are 2-D (D, rows), their boxes as many rows high as a page lets them be.
 bool encode_tmap(const TmapKey& key, CUtensorMap* m) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
-    const bool f32 = key.kind == (int)TmapKind::kF32Box32x128;
+    const bool f32 = key.kind == (int)TmapKind::kF32Box32x128, rows = key.kind == (int)TmapKind::kBf16Rows;
     const cuuint64_t esz = f32 ? 4 : 2;
-    const cuuint32_t rank = f32 ? 3 : 4;
+    const cuuint32_t rank = rows ? 2 : (f32 ? 3 : 4);
     cuuint64_t dims[4] = {(cuuint64_t)key.d0, (cuuint64_t)key.d1, (cuuint64_t)key.d2, (cuuint64_t)key.d3};
     cuuint64_t strides[3] = {(cuuint64_t)key.s1 * esz, (cuuint64_t)key.s2 * esz, (cuuint64_t)key.s3 * esz};
-    cuuint32_t box[4] = {f32 ? 32u : 64u, 128, 1, 1};
+    cuuint32_t box[4] = {f32 ? 32u : 64u, rows ? (cuuint32_t)key.d2 : 128u, 1, 1};
     cuuint32_t estr[4] = {1, 1, 1, 1};
     CUresult r = fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
                     reinterpret_cast<void*>(key.base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -100,6 +102,12 @@ bool make_tmap_bf16(CUtensorMap* m, const void* base, int B, int H, int T, int D
 bool make_tmap_f32_acc(CUtensorMap* m, const void* base, int BH, int T, int D) {
     const TmapKey key{reinterpret_cast<uintptr_t>(base), (int)TmapKind::kF32Box32x128, D, T, BH, 1,
                       (long long)D, (long long)T * D, (long long)BH * T * D};
+    return cached_tmap(m, key);
+}
+
+// A pool of the paged cache as bf16 rows; 64-column x box_rows boxes.
+bool make_tmap_rows(CUtensorMap* m, const void* base, int rows, int D, int box_rows) {
+    const TmapKey key{reinterpret_cast<uintptr_t>(base), (int)TmapKind::kBf16Rows, D, rows, box_rows, 1, (long long)D, 0, 0};
     return cached_tmap(m, key);
 }
 
@@ -523,7 +531,7 @@ int check_cache(PagedPools* c, const gpt_attn_paged_cache* a) {
     c->lens = a->lens;
     c->n_pages = a->n_pages;
     c->Hkv = a->Hkv;
-    c->page = a->page;
+    c->page = fast_div(a->page);
     c->max_pages = a->max_pages;
     c->cap = a->max_pages * a->page;
     return GPT_ATTN_OK;
@@ -551,18 +559,22 @@ int check_paged_shape(int B, int H, int Hkv, int N, int D) {
     return GPT_ATTN_OK;
 }
 
-// Blocks of the paged decode kernel: all resident at once on a B200 (148 SMs); the workspace is
-// sized by them.
-constexpr int kPagedBlocks = kPagedBlocksPerSm * 148;
+// Blocks of the paged decode kernel, one to an SM of a B200 (148), and the teams in them; the
+// workspace is sized by them.
+constexpr int kPagedBlocks = 148, kPagedAllTeams = kPagedTeams * kPagedBlocks;
 
 template <int D, int MT>
 int launch_paged(const PagedParams& p, int grid, cudaStream_t st) {
     const size_t smem = sizeof(PagedSmem<D>) + 1024;
-    if (!set_smem(paged_decode_kernel<D, MT>, smem)) return GPT_ATTN_ERR_CUDA;
-    paged_decode_kernel<D, MT><<<grid, kPagedThreads, smem, st>>>(p);
-    const int rows = p.R < 16 * MT ? p.R : 16 * MT;
+    CUtensorMap mk, mv;
+    const int rows = p.n_pages * p.Hkv * p.page.d, box = 1 << p.box_log2;
+    if (!make_tmap_rows(&mk, p.k, rows, D, box) || !make_tmap_rows(&mv, p.v, rows, D, box) ||
+        !set_smem(paged_decode_kernel<D, MT>, smem))
+        return GPT_ATTN_ERR_CUDA;
+    paged_decode_kernel<D, MT><<<grid, kPagedThreads, smem, st>>>(mk, mv, p);
+    const int item_rows = p.R < 16 * MT ? p.R : 16 * MT;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(p.B * p.Hkv * p.RB), (unsigned)((rows + kCombineWarps - 1) / kCombineWarps));
+    cfg.gridDim = dim3((unsigned)(p.B * p.Hkv * p.RB), (unsigned)((item_rows + kCombineWarps - 1) / kCombineWarps));
     cfg.blockDim = dim3(32 * kCombineWarps);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
@@ -800,7 +812,7 @@ int gpt_attn_decode(const void* q, const void* k_cache, const void* v_cache, con
 size_t gpt_attn_paged_decode_workspace_bytes(int B, int H, int Hkv, int N, int D) {
     if (check_paged_shape(B, H, Hkv, N, D) != GPT_ATTN_OK) return 0;
     const size_t rows = (size_t)16 * paged_shape(H, Hkv, N).MT;
-    return 2 * (size_t)kPagedBlocks * rows * (D + 2) * sizeof(float) + ((size_t)B + 2) * sizeof(long long);
+    return 2 * (size_t)kPagedAllTeams * rows * (D + 2) * sizeof(float) + ((size_t)B + 2) * sizeof(int);
 }
 
 int gpt_attn_paged_decode(const void* q, const gpt_attn_paged_cache* cache, const int* n_new, const int* parents,
@@ -834,25 +846,33 @@ int gpt_attn_paged_decode(const void* q, const gpt_attn_paged_cache* cache, cons
     p.q_str = st[0];
     p.o_str = st[1];
     p.part_o = static_cast<float*>(workspace);
-    p.part_ml = p.part_o + 2 * (size_t)kPagedBlocks * 16 * s.MT * D;
-    p.prefix = reinterpret_cast<long long*>(p.part_ml + 2 * (size_t)kPagedBlocks * 16 * s.MT * 2);
+    p.part_ml = p.part_o + 2 * (size_t)kPagedAllTeams * 16 * s.MT * D;
+    p.prefix = reinterpret_cast<int*>(p.part_ml + 2 * (size_t)kPagedAllTeams * 16 * s.MT * 2);
     p.B = B;
     p.H = H;
     p.Hkv = c.Hkv;
     p.G = H / c.Hkv;
     p.N = N;
+    p.by_n = fast_div(N);
     p.R = s.R;
     p.RB = s.RB;
     p.page = c.page;
+    p.box_log2 = 0;
+    while ((1 << p.box_log2) < paged_box(c.page.d)) ++p.box_log2;
     p.max_pages = c.max_pages;
     p.n_pages = c.n_pages;
     p.cap = c.cap;
     p.window = window > 0 ? window : 0;
     p.sinks = sinks > 0 && window > 0 ? sinks : 0;
-    p.scale_log2 = scale * 1.4426950408889634f;
+    p.scale_log2 = scale == 0.f ? 1.f : fabsf(scale) * 1.4426950408889634f;
+    p.q_keep = scale == 0.f ? 0u : 0xffffffffu;
+    p.q_flip = scale < 0.f ? 0x80008000u : 0u;
     p.timeout_ns = wait_timeout_ns();
-    // No more blocks than the tables can name tiles.
-    const long long most = (long long)B * c.Hkv * s.RB * ((c.cap + kPagedTile - 1) / kPagedTile);
+    // No more blocks than the tables can name tiles, the number of which has to fit an int.
+    const int tile = D == 64 ? PagedCfg<64>::kTile : PagedCfg<128>::kTile;
+    const long long items = (long long)B * c.Hkv * s.RB, tiles = (c.cap + tile - 1) / tile;
+    if (items > 0x7fffffffLL / tiles) return GPT_ATTN_ERR_SHAPE;
+    const long long most = items * tiles;
     const int grid = (int)(most < kPagedBlocks ? most : kPagedBlocks);
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     return D == 64 ? launch_paged_d<64>(p, s.MT, grid, cs) : launch_paged_d<128>(p, s.MT, grid, cs);

@@ -6,19 +6,24 @@
 // rows against the same keys, in blocks of up to 64.  A key and a value of D elements (4 D bytes)
 // serve 4 D R flops, R flops a byte, so up to some hundred rows HBM bounds the call, and the kernel
 // is built to keep loads in flight:
-//   - A producer warp brings tiles of 64 keys through a ring of shared-memory stages.  A row of a
-//     page is D * 2 contiguous bytes wherever the page lies, so 16-byte asynchronous copies by row
-//     address serve any page size; rows nobody sees are not read but zero-filled.  A tile's pages are
-//     looked up while the tile before it is issued.
+//   - Keys and values come in tiles of 32 KB (128 keys of 64 elements, 64 of 128) through a ring of
+//     shared-memory stages.  A producer warp brings them with TMA, in boxes of as many rows as a page
+//     lets them be (the largest power of two that divides it, so a tile takes 8 boxes from pages of 16
+//     tokens, 128 from odd pages), one lane to a box.  Boxes that nobody sees and missing pages are
+//     not read but zero-filled.  A tile's pages are looked up while the tile before it is issued.
 //   - All tiles of all (sequence, key head, row block) items form one list, cut into equal pieces,
-//     one to a resident block (two to an SM): ragged batches and single long sequences fill the
+//     one to a team of warps (two teams to an SM): ragged batches and single long sequences fill the
 //     GPU alike.  The ring runs on across items.  A piece that holds a whole item writes O and lse;
 //     the others leave fp32 partial results, joined by paged_combine_kernel.
-//   - Four warps compute: scores and P V on warp-level matrix instructions (16 rows x 16 keys a step;
-//     a tcgen05 tile has 128 rows, of which a call has 1 to 64), the softmax in registers between
-//     them.  In a block of 16 rows each warp takes a quarter of a tile's keys, with a softmax state of
-//     its own, joined at the end of the item; of 32 rows, each pair of warps 16 rows; of 64 rows, each
-//     warp 16 rows and all keys.
+//   - Four warps of a team compute: scores and P V on warp-level matrix instructions (16 rows x 16 keys
+//     a step; a tcgen05 tile has 128 rows, of which a call has 1 to 64), the softmax in registers
+//     between them.  With up to 16 rows each warp takes a quarter of a tile's keys, with a softmax
+//     state of its own, joined at the end of the item; with up to 32, each pair of warps 16 rows; with
+//     up to 64, each warp 16 rows and all keys.
+// A warp's steps on a tile depend on one another, so their latency counts, not their number: two teams
+// share one block because its warps can then have 208 registers each (two blocks with a producer each
+// put five warps on an SM sub-partition's registers and spilled: 90 us against 65 us at 16 streams of
+// 13 drafts, 24 query heads of 128 on 6 key heads, window 4096).
 // Statistics and accumulators are fp32; P is rounded to bf16 for the second product, as in the
 // forward kernel, while its sum is taken before the rounding.
 #pragma once
@@ -28,11 +33,13 @@
 
 namespace gpt_attn {
 
-constexpr int kPagedComputeWarps = 4;
-constexpr int kPagedCompute = 32 * kPagedComputeWarps;
-constexpr int kPagedThreads = kPagedCompute + 32;             // and the producer warp
-constexpr int kPagedBlocksPerSm = 2;
+constexpr int kPagedTeams = 2;                                // of a block
+constexpr int kPagedTeamWarps = 4;
+constexpr int kPagedTeam = 32 * kPagedTeamWarps;
+constexpr int kPagedThreads = kPagedTeams * kPagedTeam + 128; // and a warpgroup with a producer warp for each team
 constexpr int kPagedLeastTiles = 1;      // tiles of a piece at least
+// Registers of a thread: 168 at the launch, given up by the producers' warpgroup and taken by the teams.
+constexpr int kPagedProducerRegs = 88, kPagedTeamRegs = 208;
 
 struct PagedParams {
     const __nv_bfloat16* q;
@@ -45,14 +52,18 @@ struct PagedParams {
     __nv_bfloat16* o;
     float* lse;                   // [B, H, N]
     Strides q_str, o_str;         // [b, h, n, d]
-    float* part_o;                // [2 * blocks, rows of a block, D]
-    float* part_ml;               // [2 * blocks, rows of a block, 2]
-    long long* prefix;            // [B + 1] first tile of each sequence in the list, then chunk
+    float* part_o;                // [2 * teams, rows of a row block, D]
+    float* part_ml;               // [2 * teams, rows of a row block, 2]
+    int* prefix;                  // [B + 1] first tile of each sequence in the list, then chunk
     int B, H, Hkv, G, N;
+    FastDiv by_n;                 // N
     int R, RB;                    // rows of an item, row blocks
-    int page, max_pages, n_pages, cap;
+    FastDiv page;
+    int box_log2;                 // log2 of the rows that one load brings
+    int max_pages, n_pages, cap;
     int window, sinks;
-    float scale_log2;
+    float scale_log2;             // |scale| log2 e, of a scale of 0 1
+    uint32_t q_keep, q_flip;      // q & keep ^ flip: 0 for a scale of 0, -q for one below 0
     uint64_t timeout_ns;
 };
 
@@ -60,19 +71,9 @@ __device__ __forceinline__ int paged_n_new(const PagedParams& p, int b) {
     return p.n_new ? clamp_int(__ldg(p.n_new + b), 0, p.N) : p.N;
 }
 
-__device__ __forceinline__ PagedSpan paged_seq_span(const PagedParams& p, int b) {
-    return paged_span(__ldg(p.lens + b), paged_n_new(p, b), p.cap, p.window, p.sinks);
+__device__ __forceinline__ PagedSpan paged_seq_span(const PagedParams& p, int b, int tile) {
+    return paged_span(__ldg(p.lens + b), paged_n_new(p, b), p.cap, p.window, p.sinks, tile);
 }
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
-    const int bytes = valid ? 16 : 0;       // 0: the 16 bytes are zero-filled, nothing is read
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-// Arrives on `bar` once all copies that this thread has issued have landed.
-__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -84,7 +85,7 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr)
 }
 // c += a b: 16 x 16 rows by 16 x 8 columns, bf16 inputs, fp32 sums
 __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
                  "{%0, %1, %2, %3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -102,260 +103,404 @@ __device__ __forceinline__ uint32_t finite_bf16x2(uint32_t w) {
 
 template <int D>
 struct PagedCfg {
-    static constexpr int kStages = D == 64 ? 6 : 3;               // of 16 KB (D = 64), 32 KB (D = 128)
-    static constexpr int kRowBytes = D * 2;
-    static constexpr int kTileBytes = kPagedTile * kRowBytes;
+    static constexpr int kTile = D == 64 ? 128 : 64;              // keys of a tile
+    static constexpr int kWords = kTile / 32;
+    static constexpr int kTileBytes = kTile * D * 2;              // of its keys: 16 KB
+    static constexpr int kStages = 3;
+};
+
+// Byte offset of 16-byte chunk c of row r in a tile as TMA's 128-byte swizzle lays it out: 64 columns
+// of all rows after one another.
+template <int D>
+__device__ __forceinline__ uint32_t paged_at(int r, int c) {
+    return (c >> 3) * (PagedCfg<D>::kTile * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+}
+
+// A place in the list: tile t of item (sequence b, key head h, row block rb).
+struct PagedAt {
+    int b, h, rb, t;
 };
 
 // What the computing warps have to know of one tile.
 struct PagedTile {
-    unsigned long long present;   // keys of the tile that were read
-    int b, x;                     // sequence; key head * RB + row block
-    int key0, L;
-    int n_b;                      // new tokens of the sequence
-    int first, last;              // first / last tile of this block's part of the item
-    int whole;                    // the block has the whole item
-    int mask;                     // some row may not see some key that was read
+    uint32_t seen[4];             // keys of the tile that some row may see
+    int key0;                     // its first key
+    int mask;                     // some row may not see some of them
+};
+
+// One team's shared memory.
+template <int D>
+struct PagedTeam {
+    using C = PagedCfg<D>;
+    alignas(1024) uint8_t kv[C::kStages][2 * C::kTileBytes];      // keys, then values
+    PagedTile tile[C::kStages];
+    uint64_t bar_full[C::kStages], bar_empty[C::kStages];
+    uint64_t bar_join;
+    alignas(128) uint8_t q[kPagedTeamWarps][16 * 128];            // 64 columns of each warp's rows, on their way in
+    unsigned long long anc[2][kMaxNodes];                         // the tree, of alternate sequences
+    int depth[2][kMaxNodes];
+    float m[2][kPagedTeamWarps][16], l[2][kPagedTeamWarps][16];
+    int odd[2][kPagedTeamWarps];
+    PagedAt start;
 };
 
 template <int D>
 struct PagedSmem {
-    using C = PagedCfg<D>;
-    alignas(128) uint8_t kv[C::kStages][2 * C::kTileBytes];       // keys, then values
-    PagedTile tile[C::kStages];
-    uint64_t bar_full[C::kStages], bar_empty[C::kStages];
-    uint64_t bar_join;
-    unsigned long long anc[kMaxNodes];
-    int depth[kMaxNodes];
-    int parents[kMaxNodes];
-    float m[2][kPagedComputeWarps][16], l[2][kPagedComputeWarps][16];
-    __nv_bfloat16 p[kPagedComputeWarps][16 * kPagedTile];
-    int odd[2][kPagedComputeWarps];
-    long long scan[kPagedThreads / 32];
-    long long start_prefix;
-    int start_b;
+    PagedTeam<D> team[kPagedTeams];
+    int row_head[32], row_node[32];                               // row blocks of up to 32 rows: of each row
+    int scan[kPagedThreads / 32];
     int abort;
 };
 
-// Tiles of the list that sequence b contributes.
-__device__ __forceinline__ long long paged_seq_tiles(const PagedParams& p, int b) {
-    return (long long)paged_seq_span(p, b).n_tiles * p.Hkv * p.RB;
+// One of the two producer warps of a team, for its keys (which = 0) or values (1): walks the team's
+// piece of n_mine tiles, one tile a step.  Such a warp issues nearly alone, at 6 to 8 cycles an
+// instruction and some 80 a load, so instructions count here: one warp for both, with integer
+// divisions and the table's entries awaited where they were looked up, bounded the kernel.
+template <int D>
+__device__ __forceinline__ void paged_produce(const PagedParams& p, const CUtensorMap* tm, PagedTeam<D>& sm, int which,
+                                              int n_mine, const AbortCtl& ac) {
+    using C = PagedCfg<D>;
+    constexpr int kTile = C::kTile, kWords = C::kWords, kStages = C::kStages;
+    const int lane = threadIdx.x & 31;
+    PagedAt at = sm.start;
+    PagedSpan sp = paged_seq_span(p, at.b, kTile);
+    const int box = 1 << p.box_log2, boxes = kTile >> p.box_log2, past = p.n_pages * p.Hkv * p.page.d;
+    const int* table = p.table + (size_t)at.b * p.max_pages;
+    // Boxes lane, lane + 32, ... of the current tile: the table's entry (-1: nobody sees the box) and the
+    // first row within the page; the head in rows of the pool
+    int entry[kWords], in_page[kWords], h = at.h;
+    auto look_up = [&](int w) {
+        const int j = lane + w * 32, key = sp.tile(at.t) * kTile + (j << p.box_log2);
+        entry[w] = -1;
+        if (j < boxes && sp.needs_any(key, box, p.sinks)) {
+            const int page = p.page.div(key);
+            entry[w] = table[page];
+            in_page[w] = key - page * p.page.d;
+        }
+    };
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) {
+        entry[w] = -1;
+        in_page[w] = 0;
+        if (w * 32 < boxes) look_up(w);
+    }
+    int i = 0, s = -1;
+    uint32_t lap = 0;                                // parity of the stage's last release
+    for (; i < n_mine; ++i) {
+        if (++s == kStages) {
+            s = 0;
+            lap ^= 1;
+        }
+        int row[kWords];
+#pragma unroll
+        for (int w = 0; w < kWords; ++w)
+            if (w * 32 < boxes)
+                row[w] = entry[w] < 0 || entry[w] >= p.n_pages ? -1 : (entry[w] * p.Hkv + h) * p.page.d + in_page[w];
+        PagedTile d;
+        if (which == 0) {
+            d.key0 = sp.tile(at.t) * kTile;
+            // every node stands at most n - 1 past L, so keys within the window of that position are
+            // within everybody's
+            d.mask = d.key0 + kTile > sp.L || (p.window > 0 && sp.L + sp.n - 1 - d.key0 >= p.window);
+            uint32_t there[kWords];
+            bool all = d.key0 >= sp.w_lo && d.key0 + kTile <= sp.end;
+#pragma unroll
+            for (int w = 0; w < kWords; ++w) {
+                there[w] = w * 32 < boxes ? __ballot_sync(0xffffffffu, row[w] >= 0) : 0;
+                all = all && there[w] == bits_below(boxes - w * 32);
+            }
+#pragma unroll
+            for (int w = 0; w < kWords; ++w) d.seen[w] = 0xffffffffu;
+            if (!all) {
+#pragma unroll
+                for (int w = 0; w < kWords; ++w) {
+                    const int j = (lane + w * 32) >> p.box_log2;
+                    uint32_t of = there[0];
+#pragma unroll
+                    for (int x = 1; x < kWords; ++x) of = j >> 5 == x ? there[x] : of;
+                    d.seen[w] =
+                        __ballot_sync(0xffffffffu, ((of >> (j & 31)) & 1) && sp.needs(d.key0 + lane + w * 32, p.sinks));
+                }
+            }
+        }
+        // the next tile's pages
+        if (i + 1 < n_mine) {
+            if (++at.t == sp.n_tiles) {
+                at.t = 0;
+                if (++at.rb == p.RB) {
+                    at.rb = 0;
+                    if (++at.h == p.Hkv) {
+                        at.h = 0;
+                        do sp = paged_seq_span(p, ++at.b, kTile);
+                        while (sp.n_tiles == 0);
+                        table = p.table + (size_t)at.b * p.max_pages;
+                    }
+                }
+            }
+            h = at.h;
+#pragma unroll
+            for (int w = 0; w < kWords; ++w)
+                if (w * 32 < boxes) look_up(w);
+        }
+        if (i >= kStages && !warp_wait(&sm.bar_empty[s], lap ^ 1, ac)) break;
+        if (lane == 0) {
+            if (which == 0) sm.tile[s] = d;
+            mbar_arrive_expect_tx(&sm.bar_full[s], C::kTileBytes);
+        }
+        __syncwarp();
+        uint8_t* dst = sm.kv[s] + which * C::kTileBytes;
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) {
+            const int j = lane + w * 32;
+            if (w * 32 >= boxes || j >= boxes) continue;
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+                tma_load_2d(dst + c * kTile * 128 + (j << p.box_log2) * 128, tm, &sm.bar_full[s], c * 64,
+                            row[w] < 0 ? past : row[w]);
+        }
+    }
+    // the copies in flight land before the block's shared memory is given up
+    for (int j = max(0, i - kStages); j < i; ++j) mbar_wait_drain(&sm.bar_full[j % kStages], (j / kStages) & 1, p.timeout_ns);
 }
 
 template <int D, int MT>
-__global__ void __launch_bounds__(kPagedThreads, kPagedBlocksPerSm)
-paged_decode_kernel(const __grid_constant__ PagedParams p) {
+__global__ void __launch_bounds__(kPagedThreads, 1)
+paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                    const __grid_constant__ PagedParams p) {
     using C = PagedCfg<D>;
-    constexpr int kStages = C::kStages;
-    constexpr int KS = kPagedComputeWarps / MT;      // warps that share a 16-row tile's keys
-    constexpr int NT = kPagedTile / KS / 8;          // 8-key columns of a warp
+    constexpr int kStages = C::kStages, kTile = C::kTile;
+    constexpr int KS = kPagedTeamWarps / MT;         // warps that share a 16-row tile's keys
+    constexpr int kKeys = kTile / KS;                // keys of a warp in a tile
+    constexpr int NT = kKeys / 8;
     constexpr int kChunks = D / 8;                   // 16-byte chunks of a row
     constexpr int kRows = 16 * MT;
     constexpr int kWarps = kPagedThreads / 32;
     extern __shared__ uint8_t smem_raw[];
-    PagedSmem<D>& sm = *reinterpret_cast<PagedSmem<D>*>(smem_align1024(smem_raw));
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    PagedSmem<D>& block = *reinterpret_cast<PagedSmem<D>*>(smem_align1024(smem_raw));
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     asm volatile("griddepcontrol.launch_dependents;");
 
-    if (tid == 0) {
-        for (int s = 0; s < kStages; ++s) {
-            mbar_init(&sm.bar_full[s], 64);          // each producer lane: its copies, and its writes
-            mbar_init(&sm.bar_empty[s], kPagedComputeWarps);
+    if (threadIdx.x == 0) {
+        for (int g = 0; g < kPagedTeams; ++g) {
+            for (int s = 0; s < kStages; ++s) {
+                mbar_init(&block.team[g].bar_full[s], 2);          // the two producers
+                mbar_init(&block.team[g].bar_empty[s], kPagedTeamWarps);
+            }
+            mbar_init(&block.team[g].bar_join, kPagedTeamWarps);
         }
-        mbar_init(&sm.bar_join, kPagedComputeWarps);
-        sm.abort = 0;
+        block.abort = 0;
         fence_barrier_init();
     }
-    if (!p.parents && tid < p.N) {                   // one after the other: the same for all sequences
-        sm.anc[tid] = (2ull << tid) - 1;
-        sm.depth[tid] = tid;
+    if (MT < 4 && threadIdx.x < kRows) {
+        block.row_head[threadIdx.x] = p.by_n.div(threadIdx.x);
+        block.row_node[threadIdx.x] = threadIdx.x - p.by_n.div(threadIdx.x) * p.N;
+    }
+    if (!p.parents && threadIdx.x < p.N) {           // one after the other: the same for all sequences
+        for (int g = 0; g < kPagedTeams; ++g) {
+            block.team[g].anc[0][threadIdx.x] = (2ull << threadIdx.x) - 1;
+            block.team[g].depth[0][threadIdx.x] = threadIdx.x;
+        }
     }
 
-    // ---- this block's piece of the list
-    long long total = 0;
-    for (int b = tid; b < p.B; b += kPagedThreads) total += paged_seq_tiles(p, b);
+    // ---- the teams' pieces of the list.  Team g of block x is number g * blocks + x, so that short
+    // lists take an SM a piece.
+    int total = 0, mine = 0, upto = 0;               // tiles of all sequences; of sequence b, and up to its end
+    auto count = [&](int base) {
+        const int b = base + threadIdx.x;
+        mine = upto = b < p.B ? paged_seq_span(p, b, kTile).n_tiles * p.Hkv * p.RB : 0;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
-    if (lane == 0) sm.scan[warp] = total;
-    __syncthreads();
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) total += sm.scan[w];
-    const long long chunk = paged_chunk(total, gridDim.x, kPagedLeastTiles);
-    const long long begin = chunk * blockIdx.x;
-    const int n_mine = (int)max(0ll, min(chunk, total - begin));
-    {
-        long long before = 0;
-        for (int base = 0; base < p.B; base += kPagedThreads) {
-            const int b = base + tid;
-            const long long mine = b < p.B ? paged_seq_tiles(p, b) : 0;
-            long long inc = mine;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const long long y = __shfl_up_sync(0xffffffffu, inc, off);
-                if (lane >= off) inc += y;
-            }
-            __syncthreads();
-            if (lane == 31) sm.scan[warp] = inc;
-            __syncthreads();
-            inc += before;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                if (w < warp) inc += sm.scan[w];
-                before += sm.scan[w];
-            }
-            if (b < p.B && begin >= inc - mine && begin < inc) {
-                sm.start_b = b;
-                sm.start_prefix = inc - mine;
-            }
-            if (blockIdx.x == 0 && b < p.B) p.prefix[b] = inc - mine;
-        }
-        if (blockIdx.x == 0 && tid == 0) {
-            p.prefix[p.B] = total;
-            p.prefix[p.B + 1] = chunk;
+        for (int off = 1; off < 32; off <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, upto, off);
+            if (lane >= off) upto += y;
         }
         __syncthreads();
-    }
-    if (n_mine == 0) return;
-    const AbortCtl ac{&sm.abort, p.timeout_ns};
-
-    if (warp == kPagedComputeWarps) {
-        // ================ producer: walks the piece, one tile a step
-        int b = sm.start_b, x, t, first;             // item (b, x), tile t; first: this part's first tile
-        PagedSpan sp = paged_seq_span(p, b);
-        int n_b = paged_n_new(p, b);
-        {
-            const long long in_b = begin - sm.start_prefix;
-            x = (int)(in_b / sp.n_tiles);
-            t = first = (int)(in_b % sp.n_tiles);
-        }
-        // rows in the pools of this lane's two keys of the current tile
-        auto rows_of = [&](int& r0, int& r1) {
-            const int key = sp.tile(t) * kPagedTile + lane;
-            const int* table = p.table + (size_t)b * p.max_pages;
-            r0 = sp.needs(key, p.sinks) ? paged_row(table, key, p.page, p.n_pages, p.Hkv, x / p.RB) : -1;
-            r1 = sp.needs(key + 32, p.sinks) ? paged_row(table, key + 32, p.page, p.n_pages, p.Hkv, x / p.RB) : -1;
-        };
-        int r0, r1;
-        rows_of(r0, r1);
-        for (int i = 0; i < n_mine; ++i) {
-            const int s = i % kStages;
-            PagedTile d;
-            d.b = b;
-            d.x = x;
-            d.key0 = sp.tile(t) * kPagedTile;
-            d.L = sp.L;
-            d.n_b = n_b;
-            d.first = t == first;
-            d.last = i == n_mine - 1 || t == sp.n_tiles - 1;
-            d.whole = first == 0 && t == sp.n_tiles - 1;
-            // every node stands at most n - 1 past L, so keys within the window of that position are
-            // within everybody's
-            d.mask = d.key0 + kPagedTile > sp.L || (p.window > 0 && sp.L + sp.n - 1 - d.key0 >= p.window);
-            // the next tile's pages
-            int n0 = -1, n1 = -1;
-            if (i + 1 < n_mine) {
-                if (++t == sp.n_tiles) {
-                    t = first = 0;
-                    if (++x == p.Hkv * p.RB) {
-                        x = 0;
-                        do sp = paged_seq_span(p, ++b);
-                        while (sp.n_tiles == 0);
-                        n_b = sp.n;
-                    }
-                }
-                rows_of(n0, n1);
-            }
-            if (i >= kStages && !warp_wait(&sm.bar_empty[s], ((i / kStages) - 1) & 1, ac)) break;
-            d.present = __ballot_sync(0xffffffffu, r0 >= 0) | (unsigned long long)__ballot_sync(0xffffffffu, r1 >= 0) << 32;
-            if (lane == 0) sm.tile[s] = d;
-            constexpr int kAtOnce = 32 / kChunks;    // rows a warp copies at once
-            const int c = lane % kChunks;
-            const uint32_t kd = smem_u32(sm.kv[s]), vd = kd + C::kTileBytes;
-            const __nv_bfloat16 *kc = p.k + c * 8, *vc = p.v + c * 8;
+        if (lane == 31) block.scan[warp] = upto;
+        __syncthreads();
+        upto += total;
 #pragma unroll
-            for (int j = 0; j < kPagedTile / kAtOnce; ++j) {
-                const int r = j * kAtOnce + lane / kChunks;
-                const int row = __shfl_sync(0xffffffffu, j < 32 / kAtOnce ? r0 : r1, r & 31);
-                const size_t src = (size_t)max(row, 0) * D;
-                const uint32_t dst = r * C::kRowBytes + ((c ^ (r & 7)) << 4);
-                cp_async16(kd + dst, kc + src, row >= 0);
-                cp_async16(vd + dst, vc + src, row >= 0);
-            }
-            cp_async_arrive(&sm.bar_full[s]);
-            mbar_arrive(&sm.bar_full[s]);
-            r0 = n0;
-            r1 = n1;
+        for (int w = 0; w < kWarps; ++w) {
+            const int x = block.scan[w];
+            if (w < warp) upto += x;
+            total += x;
         }
-        cp_async_wait_all();
+    };
+    for (int base = 0; base < p.B; base += kPagedThreads) count(base);
+    const int chunk = paged_chunk(total, kPagedTeams * gridDim.x, kPagedLeastTiles), all = total;
+    auto find = [&](int base) {
+        const int b = base + threadIdx.x;
+        if (b >= p.B) return;
+        for (int g = 0; g < kPagedTeams; ++g) {
+            const long long begin = (long long)chunk * (g * gridDim.x + blockIdx.x);
+            if (begin >= upto - mine && begin < upto) {
+                const int n_tiles = paged_seq_span(p, b, kTile).n_tiles;
+                const int in_b = (int)begin - (upto - mine), x = in_b / n_tiles;
+                block.team[g].start = PagedAt{b, x / p.RB, x % p.RB, in_b - x * n_tiles};
+            }
+        }
+        if (blockIdx.x == 0) p.prefix[b] = upto - mine;
+    };
+    if (p.B <= kPagedThreads) {
+        find(0);
+    } else {
+        total = 0;
+        for (int base = 0; base < p.B; base += kPagedThreads) {
+            count(base);
+            find(base);
+        }
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        p.prefix[p.B] = all;
+        p.prefix[p.B + 1] = chunk;
+    }
+    __syncthreads();
+
+    // warps of team 0, of team 1, then keys' and values' producers of team 0, of team 1
+    static_assert(kPagedTeams == 2, "two producers to a team make a warpgroup");
+    const int extra = warp - kPagedTeams * kPagedTeamWarps;
+    const int g = extra < 0 ? warp / kPagedTeamWarps : extra / 2;
+    const int team_no = g * gridDim.x + blockIdx.x;
+    const int n_mine = (int)max(0ll, min((long long)chunk, all - (long long)chunk * team_no));
+    const AbortCtl ac{&block.abort, p.timeout_ns};
+    if (extra >= 0) {
+        regs_dec<kPagedProducerRegs>();
+        if (n_mine > 0) paged_produce<D>(p, extra & 1 ? &tm_v : &tm_k, block.team[g], extra & 1, n_mine, ac);
         return;
     }
+    regs_inc<kPagedTeamRegs>();
+    if (n_mine == 0) return;
+    PagedTeam<D>& sm = block.team[g];
+    const int tid = threadIdx.x - g * kPagedTeam, w4 = warp - g * kPagedTeamWarps;
 
-    // ================ computing warps
     // state of the current item: two rows per thread (r and r + 8 of the warp's 16)
-    const int mt = warp / KS, ks = warp % KS;
+    const int mt = w4 / KS, ks = w4 % KS;
+    const int kb = ks * kKeys;                       // first key of the warp within a tile
+    const int r_lo = mt * 16 + (lane >> 2);
     uint32_t qf[D / 16][4];
     float oacc[D / 8][4];
     float m[2], l[2];
-    int pos[2];
-    unsigned long long anc[2];
-    int cur_b = -1, part_i = 0, item = 0;            // part_i: the part's first tile
-    const int r_lo = mt * 16 + (lane >> 2);
-    uint32_t joins = 0;
-    // a barrier of the computing warps
+    int lower[2];
+    unsigned long long vis[2];                       // 0: no such row, or no such node
+    int node[2] = {0, 0}, head[2] = {0, 0};          // node, and head within the group, of the two rows; -1: no row
+    int cur_b = -1, cur_rb = -1, item = 0, tree = 0;
+    uint32_t joins = 0, lap = 1;
+    int s = -1;
+    // a barrier of the team
     auto join = [&]() -> bool {
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.bar_join);
         return warp_wait(&sm.bar_join, joins++ & 1, ac);
     };
-
-    for (int i = 0; i < n_mine; ++i) {
-        const int s = i % kStages;
-        if (!warp_wait(&sm.bar_full[s], (i / kStages) & 1, ac)) return;
-        const PagedTile t = sm.tile[s];
-        const int h = t.x / p.RB, rb = t.x - h * p.RB;
-        if (t.first) {
-            part_i = i;
-            if (p.parents && t.b != cur_b) {
-                // the tree of this sequence
-                cur_b = t.b;
-                if (!join()) return;                 // the last sequence's is no longer read
-                if (tid < p.N) sm.parents[tid] = __ldg(p.parents + (size_t)t.b * p.N + tid);
-                if (!join()) return;
-                if (tid < p.N) {
-                    const unsigned long long a = paged_ancestors(tid, sm.parents);
-                    sm.anc[tid] = a;
-                    sm.depth[tid] = __popcll(a) - 1;
+    PagedAt at = sm.start;
+    int first = at.t, part_i = 0;                    // the part's first tile within the item and the piece
+    PagedSpan sp = paged_seq_span(p, at.b, kTile);
+    // The item's rows, before its first tile is waited for.
+    auto set_up = [&]() -> bool {
+        // the rows, 16 bytes a lane, before anything that waits
+        uint4 raw[D / 64][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int r = at.rb * 64 + mt * 16 + j * 4 + (lane >> 3), hd = p.by_n.div(r), nd = r - hd * p.N;
+            const bool live = r < p.R && nd < sp.n;
+            const __nv_bfloat16* src = p.q + at.b * p.q_str.b + (long long)(at.h * p.G + hd) * p.q_str.h + nd * p.q_str.t +
+                                       (lane & 7) * 8;
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+                raw[c][j] = live ? __ldg(reinterpret_cast<const uint4*>(src + c * 64)) : make_uint4(0u, 0u, 0u, 0u);
+        }
+        if (p.parents && at.b != cur_b) {
+            // The tree of this sequence, by the first warp: each node takes over the ancestors of the node
+            // it points at and points where that one does, so 6 rounds reach 64 nodes up.  The other
+            // buffer may still be read; the one before it is not, since all have passed that tree's join.
+            tree ^= cur_b >= 0;
+            cur_b = at.b;
+            if (w4 == 0) {
+                unsigned long long a[2];
+                int up[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int n = lane + 32 * e, to = n < p.N ? __ldg(p.parents + (size_t)at.b * p.N + n) : -1;
+                    a[e] = 1ull << n;
+                    up[e] = to < n ? to : -1;
                 }
-                if (!join()) return;
+#pragma unroll 1
+                for (int step = 1; step < p.N; step *= 2) {
+                    unsigned long long more[2];
+                    int next[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int from = max(up[e], 0);
+                        const unsigned long long a0 = __shfl_sync(0xffffffffu, a[0], from & 31),
+                                                 a1 = __shfl_sync(0xffffffffu, a[1], from & 31);
+                        const int u0 = __shfl_sync(0xffffffffu, up[0], from & 31), u1 = __shfl_sync(0xffffffffu, up[1], from & 31);
+                        more[e] = up[e] < 0 ? 0 : (from < 32 ? a0 : a1);
+                        next[e] = up[e] < 0 ? -1 : (from < 32 ? u0 : u1);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        a[e] |= more[e];
+                        up[e] = next[e];
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    sm.anc[tree][lane + 32 * e] = a[e];
+                    sm.depth[tree][lane + 32 * e] = __popcll(a[e]) - 1;
+                }
             }
+            if (!join()) return false;
+        }
+        if (at.rb != cur_rb) {
+            cur_rb = at.rb;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int r = rb * 64 + r_lo + 8 * e;
-                const int node = r % p.N;
-                const bool live = r < p.R && node < t.n_b;
-                anc[e] = live ? sm.anc[node] : 0;
-                pos[e] = t.L + sm.depth[node];
-                m[e] = -INFINITY;
-                l[e] = 0.f;
-                const __nv_bfloat16* src = p.q + t.b * p.q_str.b + (long long)(h * p.G + (live ? r / p.N : 0)) * p.q_str.h +
-                                           node * p.q_str.t + (lane & 3) * 2;
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    qf[kk][e] = live ? *reinterpret_cast<const uint32_t*>(src + kk * 16) : 0u;
-                    qf[kk][e + 2] = live ? *reinterpret_cast<const uint32_t*>(src + kk * 16 + 8) : 0u;
-                }
+                const int r = at.rb * 64 + r_lo + 8 * e, hd = p.by_n.div(r);
+                head[e] = r < p.R ? hd : -1;
+                node[e] = r - hd * p.N;
             }
-#pragma unroll
-            for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) oacc[n][e] = 0.f;
         }
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int r = j * 4 + (lane >> 3);
+                *reinterpret_cast<uint4*>(sm.q[w4] + r * 128 + (((lane & 7) ^ (r & 7)) << 4)) = raw[c][j];
+            }
+            __syncwarp();
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+                uint32_t(&a)[4] = qf[c * 4 + kk];
+                ldmatrix4(a, smem_u32(sm.q[w4]) + (lane & 15) * 128 + (((kk * 2 + (lane >> 4)) ^ (lane & 7)) << 4));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) a[e] = a[e] & p.q_keep ^ p.q_flip;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const bool live = head[e] >= 0 && node[e] < sp.n;
+            const int pos = sp.L + sm.depth[tree][node[e]];
+            lower[e] = paged_lower(pos, p.window);
+            vis[e] = live ? paged_visible(sm.anc[tree][node[e]], pos, sm.depth[tree], sp.L, p.window, p.sinks) : 0;
+            m[e] = -INFINITY;
+            l[e] = 0.f;
+        }
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) oacc[n][e] = 0.f;
+        return true;
+    };
+    if (!set_up()) return;
+
+    for (int i = 0; i < n_mine; ++i) {
+        if (++s == kStages) s = 0;
+        if (s == 0) lap ^= 1;
+        if (!warp_wait(&sm.bar_full[s], lap, ac)) return;
+        const PagedTile& t = sm.tile[s];
 
         // ---- scores of this warp's keys
-        const uint8_t* kt = sm.kv[s];
-        const uint8_t* vt = sm.kv[s] + C::kTileBytes;
-        const int kb = ks * (kPagedTile / KS);        // first key of the warp within the tile
+        const uint32_t k_addr = smem_u32(sm.kv[s]), v_addr = k_addr + C::kTileBytes;
+        uint8_t* vt = sm.kv[s] + C::kTileBytes;
         float sc[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -363,37 +508,46 @@ paged_decode_kernel(const __grid_constant__ PagedParams p) {
             for (int e = 0; e < 4; ++e) sc[n][e] = 0.f;
         {
             const int key = kb + (lane & 7) + ((lane >> 4) << 3);
-            const uint32_t base = smem_u32(kt) + key * C::kRowBytes;
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
-                const int c = kk * 2 + ((lane >> 3) & 1);
+                const uint32_t at = k_addr + paged_at<D>(key, kk * 2 + ((lane >> 3) & 1));
 #pragma unroll
                 for (int n = 0; n < NT; n += 2) {
                     uint32_t b4[4];
-                    ldmatrix4(b4, base + n * 8 * C::kRowBytes + ((c ^ (key & 7)) << 4));
+                    ldmatrix4(b4, at + n * 8 * 128);
                     mma_16816(sc[n], qf[kk], b4[0], b4[1]);
                     mma_16816(sc[n + 1], qf[kk], b4[2], b4[3]);
                 }
             }
         }
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sc[n][e] *= p.scale_log2;
         // keys behind the cached tokens, at a window's edge or on missing pages; rows of nodes that
         // do not exist see nothing anywhere, which the end of the item takes care of
-        if (t.mask || ~t.present) {
+        const int mask = t.mask;
+        uint32_t seen[(kKeys + 31) / 32];            // of the warp's keys
+        bool full = true;
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+        for (int w = 0; w < (kKeys + 31) / 32; ++w) {
+            seen[w] = t.seen[kb / 32 + w] >> (kb & 31);
+            full = full && (kKeys < 32 ? (~seen[w] & ((1u << (kKeys & 31)) - 1)) == 0 : seen[w] == 0xffffffffu);
+        }
+        if (mask || !full) {
+            const int key0 = t.key0 + kb;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int key = kb + n * 8 + (lane & 3) * 2 + (e & 1);
-                    const bool see = ((t.present >> key) & 1) && paged_sees(t.key0 + key, pos[e >> 1], anc[e >> 1], sm.depth,
-                                                                           t.L, p.window, p.sinks);
-                    sc[n][e] = see ? sc[n][e] : -INFINITY;
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int w = 0; w < (NT + 3) / 4; ++w) {
+                    // this lane's keys of the word: bits 0 and 1, 8 and 9, ...
+                    const uint32_t see = (seen[w] & paged_sees(key0 + w * 32, sp.L, lower[e], p.sinks, vis[e])) >>
+                                         ((lane & 3) * 2);
+#pragma unroll
+                    for (int n = 0; n < 4 && w * 4 + n < NT; ++n)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+                            if (!((see >> (n * 8 + x)) & 1)) sc[w * 4 + n][2 * e + x] = -INFINITY;
                 }
         }
-        // ---- online softmax: rescaled only where a row's maximum grows by more than 2^8
+        // ---- online softmax: rescaled only where a row's maximum grows by more than 2^8.  The scale is
+        // above 0 (its sign is q's), so it is applied to the maximum, and to the scores within the exponent.
         float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -403,7 +557,7 @@ paged_decode_kernel(const __grid_constant__ PagedParams p) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
-            mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
+            mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2)) * p.scale_log2;
         }
         const bool grow0 = mx[0] > m[0] + kLazyRescale, grow1 = mx[1] > m[1] + kLazyRescale;
         if (__any_sync(0xffffffffu, grow0 || grow1)) {
@@ -424,31 +578,44 @@ paged_decode_kernel(const __grid_constant__ PagedParams p) {
         uint32_t pf[NT / 2][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const float p0 = ex2_approx(sc[n][0] - mu0), p1 = ex2_approx(sc[n][1] - mu0);
-            const float p2 = ex2_approx(sc[n][2] - mu1), p3 = ex2_approx(sc[n][3] - mu1);
+            const float p0 = ex2_approx(fmaf(sc[n][0], p.scale_log2, -mu0)), p1 = ex2_approx(fmaf(sc[n][1], p.scale_log2, -mu0));
+            const float p2 = ex2_approx(fmaf(sc[n][2], p.scale_log2, -mu1)), p3 = ex2_approx(fmaf(sc[n][3], p.scale_log2, -mu1));
             l[0] += p0 + p1;
             l[1] += p2 + p3;
             pf[n / 2][(n & 1) * 2] = pack_bf16x2(p0, p1);
             pf[n / 2][(n & 1) * 2 + 1] = pack_bf16x2(p2, p3);
         }
+        // Rows that came along in a box without being seen may hold anything: their values are cleared,
+        // by every warp for itself.
+        if (!full) {
+            for (int c = lane; c < kKeys * kChunks; c += 32) {
+                const int key = c / kChunks;
+                if (!((t.seen[(kb + key) >> 5] >> ((kb + key) & 31)) & 1))
+                    *reinterpret_cast<uint4*>(vt + paged_at<D>(kb + key, c % kChunks)) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            __syncwarp();
+        }
         // New tokens that are not every node's ancestors may hold infinities or NaN, which must not
         // reach the others through 0 * NaN.  Where a tile holds some, they are added to the rows with
         // P > 0 one by one and then cleared in the stage.
-        if (t.mask && p.N > 1) {
-            uint4* rows = reinterpret_cast<uint4*>(sm.kv[s] + C::kTileBytes);
+        if (mask && p.N > 1) {
+            uint4* rows = reinterpret_cast<uint4*>(vt);
             bool odd = false;
 #pragma unroll 4
-            for (int c = tid; c < kPagedTile * kChunks; c += kPagedCompute) {
+            for (int c = tid; c < kTile * kChunks; c += kPagedTeam) {
+                const int key = (c >> 3) & (kTile - 1);
                 const uint4 x = rows[c];
-                odd = odd || not_finite(x.x) || not_finite(x.y) || not_finite(x.z) || not_finite(x.w);
+                if ((t.seen[key >> 5] >> (key & 31)) & 1)
+                    odd = odd || not_finite(x.x) || not_finite(x.y) || not_finite(x.z) || not_finite(x.w);
             }
             odd = __any_sync(0xffffffffu, odd);
-            int(&all)[kPagedComputeWarps] = sm.odd[joins & 1];    // a warp may be a join ahead of the readers
-            if (lane == 0) all[warp] = odd;
+            int(&any)[kPagedTeamWarps] = sm.odd[joins & 1];       // a warp may be a join ahead of the readers
+            if (lane == 0) any[w4] = odd;
             if (!join()) return;
-            odd = all[0] | all[1] | all[2] | all[3];
+            odd = any[0] | any[1] | any[2] | any[3];
             if (odd) {
-                __nv_bfloat16(*pw)[NT * 8] = reinterpret_cast<__nv_bfloat16(*)[NT * 8]>(sm.p[warp]);
+                // P through the stage's keys, which all warps have read
+                __nv_bfloat16(*pw)[kKeys] = reinterpret_cast<__nv_bfloat16(*)[kKeys]>(sm.kv[s]) + w4 * 16;
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -459,10 +626,8 @@ paged_decode_kernel(const __grid_constant__ PagedParams p) {
 #pragma unroll
                 for (int n = 0; n < D / 8; ++n)
 #pragma unroll 1
-                    for (int kk = 0; kk < NT * 8; ++kk) {
-                        const int key = kb + kk;
-                        const uint32_t w = *reinterpret_cast<const uint32_t*>(
-                            vt + key * C::kRowBytes + ((n ^ (key & 7)) << 4) + (lane & 3) * 4);
+                    for (int kk = 0; kk < kKeys; ++kk) {
+                        const uint32_t w = *reinterpret_cast<const uint32_t*>(vt + paged_at<D>(kb + kk, n) + (lane & 3) * 4);
                         if (!not_finite(w)) continue;
                         const float x0 = __uint_as_float(w << 16), x1 = __uint_as_float(w & 0xffff0000u);
 #pragma unroll
@@ -473,7 +638,7 @@ paged_decode_kernel(const __grid_constant__ PagedParams p) {
                         }
                     }
                 if (!join()) return;
-                for (int c = tid; c < kPagedTile * kChunks; c += kPagedCompute) {
+                for (int c = tid; c < kTile * kChunks; c += kPagedTeam) {
                     uint4 x = rows[c];
                     x.x = finite_bf16x2(x.x);
                     x.y = finite_bf16x2(x.y);
@@ -487,38 +652,34 @@ paged_decode_kernel(const __grid_constant__ PagedParams p) {
         // ---- O += P V
         {
             const int key = kb + (lane & 15);
-            const uint32_t base = smem_u32(vt) + key * C::kRowBytes;
 #pragma unroll
             for (int kk = 0; kk < NT / 2; ++kk) {
 #pragma unroll
                 for (int n = 0; n < D / 16; ++n) {
-                    const int c = n * 2 + (lane >> 4);
                     uint32_t b4[4];
-                    ldmatrix4_trans(b4, base + kk * 16 * C::kRowBytes + ((c ^ (key & 7)) << 4));
+                    ldmatrix4_trans(b4, v_addr + paged_at<D>(key, n * 2 + (lane >> 4)) + kk * 16 * 128);
                     mma_16816(oacc[2 * n], pf[kk], b4[0], b4[1]);
                     mma_16816(oacc[2 * n + 1], pf[kk], b4[2], b4[3]);
                 }
             }
         }
 
-        if (t.last) {
-            // ---- end of the item (or of this block's part)
+        const bool done = at.t == sp.n_tiles - 1;
+        if (done || i == n_mine - 1) {
+            // ---- end of the item (or of this team's part)
+            const int b = at.b, h = at.h;
+            const bool whole = done && first == 0;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
                 l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
-                if (anc[e] == 0) {                   // a row or node that does not exist sees nothing
+                if (vis[e] == 0) {                   // a row or node that does not exist sees nothing
                     m[e] = -INFINITY;
                     l[e] = 0.f;
                 }
             }
             // a piece has at most two partial items: the one it starts in and the one it ends in
-            const size_t part = (2 * (size_t)blockIdx.x + (part_i > 0)) * kRows;
-            auto out_row = [&](int r, int& head, int& node) {
-                head = h * p.G + (rb * 64 + r) / p.N;
-                node = (rb * 64 + r) % p.N;
-                return p.o + t.b * p.o_str.b + (long long)head * p.o_str.h + node * p.o_str.t;
-            };
+            const size_t part = (2 * (size_t)team_no + (part_i > 0)) * kRows;
             if constexpr (KS > 1) {
                 // The warps that share rows join their states through the stage itself, which they
                 // have all read by then.  (The statistics alternate between two buffers: a warp may
@@ -527,24 +688,23 @@ paged_decode_kernel(const __grid_constant__ PagedParams p) {
                 if ((lane & 3) == 0) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        sm.m[par][warp][(lane >> 2) + 8 * e] = m[e];
-                        sm.l[par][warp][(lane >> 2) + 8 * e] = l[e];
+                        sm.m[par][w4][(lane >> 2) + 8 * e] = m[e];
+                        sm.l[par][w4][(lane >> 2) + 8 * e] = l[e];
                     }
                 }
                 if (!join()) return;
-                float2* mine = reinterpret_cast<float2*>(sm.kv[s]) + (size_t)warp * 16 * (D / 2);
+                float2* state = reinterpret_cast<float2*>(sm.kv[s]);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int r = (lane >> 2) + 8 * e;
-                    if (anc[e] == 0) continue;
+                    if (vis[e] == 0) continue;
 #pragma unroll
                     for (int n = 0; n < D / 8; ++n)
-                        mine[r * (D / 2) + ((n * 4 + (lane & 3)) ^ ((r & 3) * 4))] =
+                        state[(w4 * 16 + r) * (D / 2) + ((n * 4 + (lane & 3)) ^ ((r & 3) * 4))] =
                             make_float2(oacc[n][2 * e], oacc[n][2 * e + 1]);
                 }
                 if (!join()) return;
-                const int n_rows = min(p.R - rb * 64, kRows);
-                for (int at = tid; at < n_rows * (D / 4); at += kPagedCompute) {
+                for (int at = tid; at < p.R * (D / 4); at += kPagedTeam) {       // R <= kRows: one row block
                     const int r = at / (D / 4), c = at % (D / 4);
                     const int w0 = (r / 16) * KS, rr = r % 16;
                     float M = -INFINITY, sum = 0.f;
@@ -555,27 +715,25 @@ paged_decode_kernel(const __grid_constant__ PagedParams p) {
 #pragma unroll
                     for (int w = 0; w < KS; ++w) {
                         const float lw = sm.l[par][w0 + w][rr];
+                        if (lw == 0.f) continue;     // a warp whose keys the row does not see wrote nothing of use
                         const float f = ex2_approx(sm.m[par][w0 + w][rr] - mu);
-                        sum += lw == 0.f ? 0.f : lw * f;
-                        if (lw != 0.f) {             // a warp whose keys the row does not see wrote nothing of use
-                            const float4 y = *reinterpret_cast<const float4*>(
-                                reinterpret_cast<const float2*>(sm.kv[s]) + (size_t)(w0 + w) * 16 * (D / 2) + rr * (D / 2) +
-                                ((c * 2) ^ ((rr & 3) * 4)));
-                            a.x += f * y.x;
-                            a.y += f * y.y;
-                            a.z += f * y.z;
-                            a.w += f * y.w;
-                        }
+                        sum += lw * f;
+                        const float4 y = *reinterpret_cast<const float4*>(state + ((w0 + w) * 16 + rr) * (D / 2) +
+                                                                          ((c * 2) ^ ((rr & 3) * 4)));
+                        a.x += f * y.x;
+                        a.y += f * y.y;
+                        a.z += f * y.z;
+                        a.w += f * y.w;
                     }
                     const bool any = sum != 0.f;
-                    if (t.whole) {
-                        int head, node;
-                        __nv_bfloat16* dst = out_row(r, head, node) + c * 4;
+                    if (whole) {
+                        const int hd = h * p.G + block.row_head[r], nd = block.row_node[r];
+                        __nv_bfloat16* dst = p.o + b * p.o_str.b + hd * p.o_str.h + nd * p.o_str.t + c * 4;
                         const float inv = any ? 1.f / sum : 0.f;
                         *reinterpret_cast<uint2*>(dst) =
                             make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
                         if (c == 0)
-                            p.lse[((size_t)t.b * p.H + head) * p.N + node] =
+                            p.lse[((size_t)b * p.H + hd) * p.N + nd] =
                                 any ? (M + log2f(sum)) * 0.69314718055994531f : -INFINITY;
                     } else {
                         *reinterpret_cast<float4*>(p.part_o + (part + r) * D + c * 4) = a;
@@ -586,18 +744,18 @@ paged_decode_kernel(const __grid_constant__ PagedParams p) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int r = r_lo + 8 * e;
-                    if (rb * 64 + r >= p.R) continue;
+                    if (head[e] < 0) continue;
                     const bool any = l[e] != 0.f;
-                    if (t.whole) {
-                        int head, node;
-                        __nv_bfloat16* dst = out_row(r, head, node) + (lane & 3) * 2;
+                    if (whole) {
+                        const int hd = h * p.G + head[e];
+                        __nv_bfloat16* dst = p.o + b * p.o_str.b + hd * p.o_str.h + node[e] * p.o_str.t + (lane & 3) * 2;
                         const float inv = any ? 1.f / l[e] : 0.f;
 #pragma unroll
                         for (int n = 0; n < D / 8; ++n)
                             *reinterpret_cast<uint32_t*>(dst + n * 8) =
                                 any ? pack_bf16x2(oacc[n][2 * e] * inv, oacc[n][2 * e + 1] * inv) : 0u;
                         if ((lane & 3) == 0)
-                            p.lse[((size_t)t.b * p.H + head) * p.N + node] =
+                            p.lse[((size_t)b * p.H + hd) * p.N + node[e]] =
                                 any ? (m[e] + log2f(l[e])) * 0.69314718055994531f : -INFINITY;
                     } else {
                         float* dst = p.part_o + (part + r) * D + (lane & 3) * 2;
@@ -609,9 +767,25 @@ paged_decode_kernel(const __grid_constant__ PagedParams p) {
                     }
                 }
             }
+            fence_proxy_async_smem();                // what was written into the stage comes before the next copies
         }
+        if (mask || !full) fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.bar_empty[s]);
+        ++at.t;
+        if (done && i + 1 < n_mine) {
+            at.t = first = 0;
+            part_i = i + 1;
+            if (++at.rb == p.RB) {
+                at.rb = 0;
+                if (++at.h == p.Hkv) {
+                    at.h = 0;
+                    do sp = paged_seq_span(p, ++at.b, kTile);
+                    while (sp.n_tiles == 0);
+                }
+            }
+            if (!set_up()) return;
+        }
     }
 }
 
@@ -633,13 +807,13 @@ paged_combine_kernel(const __grid_constant__ PagedParams p) {
     const int r = blockIdx.y * kCombineWarps + (threadIdx.x >> 5);
     const int c = lane % kPerRow, g = lane / kPerRow;
     if (rb * 64 + r >= p.R) return;
-    const long long chunk = p.prefix[p.B + 1], in_b = p.prefix[b];
-    const int n_tiles = paged_seq_span(p, b).n_tiles;
-    const long long first = in_b + (long long)x * n_tiles;
+    const int chunk = p.prefix[p.B + 1], in_b = p.prefix[b];
+    const int n_tiles = paged_seq_span(p, b, PagedCfg<D>::kTile).n_tiles;
+    const int first = in_b + x * n_tiles;
     float M = -INFINITY, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     if (n_tiles > 0) {
-        const int from = (int)(first / chunk), to = (int)((first + n_tiles - 1) / chunk);
+        const int from = first / chunk, to = (first + n_tiles - 1) / chunk;
         if (from == to) return;                        // one block had the whole item
         auto row_of = [&](int s) { return (2 * (size_t)s + (first > s * chunk)) * kRows + r; };
         for (int s = from + lane; s <= to; s += 32) M = fmaxf(M, p.part_ml[row_of(s) * 2]);

@@ -24,7 +24,8 @@ struct PagedPools {
     __nv_bfloat16* v;
     const int* table;             // [B, max_pages]
     const int* lens;              // [B]
-    int n_pages, Hkv, page, max_pages, cap;
+    int n_pages, Hkv, max_pages, cap;
+    FastDiv page;
 };
 
 // ------------------------------------------------------------------------------- rows of tokens

@@ -8,45 +8,56 @@
 
 namespace gpt_attn {
 
-constexpr int kPagedTile = 64;       // keys per tile of the paged decode kernel
+constexpr int kPagedBox = 64;         // rows that one load brings at most
 constexpr int kMaxNodes = 64;        // new tokens of a sequence in one call (one bit each)
 
 GPT_ATTN_HD int clamp_int(int x, int lo, int hi) { return x < lo ? lo : (x > hi ? hi : x); }
 
+// Division of 0 <= n < 2^31 by a constant d >= 1 as a multiplication and a shift: with l = ceil(log2 d)
+// and m = floor(2^(31 + l) / d) + 1, m d = 2^(31 + l) + e with 0 < e <= d <= 2^l, and n m / 2^(31 + l) is
+// n / d plus n e / (d 2^(31 + l)) < 1 / d, which does not reach the next whole number.
+struct FastDiv {
+    unsigned long long m;
+    int shift, d;
+    GPT_ATTN_HD int div(int n) const { return (int)((unsigned long long)(unsigned)n * m >> shift); }
+};
+
+GPT_ATTN_HD FastDiv fast_div(int d) {
+    int l = 0;
+    while (l < 31 && (1ll << l) < d) ++l;
+    FastDiv f;
+    f.shift = 31 + l;
+    f.m = (1ull << f.shift) / (unsigned)d + 1;
+    f.d = d;
+    return f;
+}
+
 // What the new tokens of one sequence visit: L cached tokens (clamped to the table's capacity), n
 // new ones behind them.  The node at depth 0 stands at position L, so with a window the cached
 // keys in use are [w_lo, L) and the sinks before them; the new tokens' own keys are [L, end).
-// Tiles of 64 keys: ns sink tiles from 0 on, then [t_lo, t_lo + n_tiles - ns).
+// Tiles of `tile` keys: ns sink tiles from 0 on, then [t_lo, t_lo + n_tiles - ns).
 struct PagedSpan {
     int L, n, end, w_lo, ns, t_lo, n_tiles;
     GPT_ATTN_HD int tile(int i) const { return i < ns ? i : t_lo + (i - ns); }
     // Whether the key's row has to be read at all.
     GPT_ATTN_HD bool needs(int key, int sinks) const { return key < end && (key >= w_lo || key < sinks); }
+    // The same for any of `n` keys from `key` on.
+    GPT_ATTN_HD bool needs_any(int key, int n, int sinks) const {
+        return key < end && (key + n > w_lo || key < sinks);
+    }
 };
 
-GPT_ATTN_HD PagedSpan paged_span(int len, int n_new, int cap, int window, int sinks) {
+GPT_ATTN_HD PagedSpan paged_span(int len, int n_new, int cap, int window, int sinks, int tile) {
     PagedSpan s;
     s.L = clamp_int(len, 0, cap);
     s.n = n_new;
     s.end = s.L + n_new < cap ? s.L + n_new : cap;
     s.w_lo = window > 0 && s.L - window + 1 > 0 ? s.L - window + 1 : 0;
-    s.t_lo = s.w_lo / kPagedTile;
-    s.ns = (int)(((long long)sinks + kPagedTile - 1) / kPagedTile);
+    s.t_lo = s.w_lo / tile;
+    s.ns = (int)(((long long)sinks + tile - 1) / tile);
     if (s.ns > s.t_lo) s.ns = s.t_lo;
-    s.n_tiles = s.n > 0 && s.end > 0 ? s.ns + (s.end - 1) / kPagedTile - s.t_lo + 1 : 0;
+    s.n_tiles = s.n > 0 && s.end > 0 ? s.ns + (s.end - 1) / tile - s.t_lo + 1 : 0;
     return s;
-}
-
-// Whether the node at position `pos` with ancestors `anc` (bit d: new token d, itself included)
-// sees key `key`; a new token d stands at L + depth[d].
-GPT_ATTN_HD bool paged_sees(int key, int pos, unsigned long long anc, const int* depth, int L, int window, int sinks) {
-    int x = key;
-    if (key >= L) {
-        const int d = key - L;
-        if (d >= kMaxNodes || !((anc >> d) & 1)) return false;
-        x = L + depth[d];
-    }
-    return window <= 0 || pos - x < window || x < sinks;
 }
 
 // Ancestors (itself included) of node i, by its parents; a parent that is not before its child
@@ -60,17 +71,50 @@ GPT_ATTN_HD unsigned long long paged_ancestors(int i, const int* parents) {
     return m;
 }
 
+// New tokens that the node at position `pos` with ancestors `anc` (bit d: new token d, itself included)
+// sees; new token d stands at L + depth[d].
+GPT_ATTN_HD unsigned long long paged_visible(unsigned long long anc, int pos, const int* depth, int L, int window,
+                                             int sinks) {
+    if (window <= 0 || pos - L < window) return anc;          // the window reaches back to the first of them
+    unsigned long long vis = 0;
+    for (int d = 0; d < kMaxNodes; ++d)
+        if (((anc >> d) & 1) && (pos - (L + depth[d]) < window || L + depth[d] < sinks)) vis |= 1ull << d;
+    return vis;
+}
+
+// First position within the window of a node at `pos`.
+GPT_ATTN_HD int paged_lower(int pos, int window) { return window > 0 && pos - window + 1 > 0 ? pos - window + 1 : 0; }
+
+// The lowest n bits.
+GPT_ATTN_HD unsigned bits_below(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1); }
+
+// Which of the keys [key0, key0 + 32) a node sees: cached ones by their positions, new ones by the
+// node's visible ones.
+GPT_ATTN_HD unsigned paged_sees(int key0, int L, int lower, int sinks, unsigned long long vis) {
+    const int at = L - key0;                                  // the bit of new token 0
+    const unsigned cached = bits_below(at) & (~bits_below(lower - key0) | bits_below(sinks - key0));
+    if (at >= 32 || at <= -kMaxNodes) return cached;
+    return cached | (unsigned)(at >= 0 ? vis << at : vis >> -at);
+}
+
 // Row of position `key` of a sequence within a pool [n_pages, Hkv, page, D], in rows of D; -1 if
 // its page is missing.
-GPT_ATTN_HD int paged_row(const int* table_row, int key, int page, int n_pages, int Hkv, int h) {
-    const int e = table_row[key / page];
-    return e < 0 || e >= n_pages ? -1 : (e * Hkv + h) * page + key % page;
+GPT_ATTN_HD int paged_row(const int* table_row, int key, const FastDiv& page, int n_pages, int Hkv, int h) {
+    const int j = page.div(key), e = table_row[j];
+    return e < 0 || e >= n_pages ? -1 : (e * Hkv + h) * page.d + (key - j * page.d);
+}
+
+// Rows of a page that one load brings: the largest power of two that divides the page, up to
+// kPagedBox, so that a box begins and ends within a page and within a tile.
+GPT_ATTN_HD int paged_box(int page) {
+    int box = page & -page;
+    return box < kPagedBox ? box : kPagedBox;
 }
 
 // The flattened list of tiles of all items is cut into pieces of `chunk` tiles, one to a block;
 // at least `least` to a piece, so that short calls are not scattered.
-GPT_ATTN_HD long long paged_chunk(long long total, int blocks, int least) {
-    const long long c = (total + blocks - 1) / blocks;
+GPT_ATTN_HD int paged_chunk(int total, int blocks, int least) {
+    const int c = total / blocks + (total % blocks > 0);
     return c < least ? least : c;
 }
 

@@ -24,6 +24,7 @@ namespace gpt_attn {
 enum class TmapKind : int {
     kBf16Box64x128 = 1,    // bf16 4-D (D, T, H, B) with strides, 64-column x 128-row boxes, 128-byte swizzle
     kF32Box32x128 = 2,     // fp32 3-D (D, T, B*H) contiguous, 32-column x 128-row boxes, 128-byte swizzle
+    kBf16Rows = 3,         // bf16 2-D (D, rows) contiguous, 64-column x d2-row boxes, 128-byte swizzle
 };
 
 struct TmapKey {

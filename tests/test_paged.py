@@ -82,10 +82,7 @@ def S(tmp_path_factory):
     subprocess.run([cxx, "-std=c++17", "-O1", "-shared", "-fPIC", "-I",
                     os.path.join(ROOT, "causal_attention_sdpa_b200", "csrc"),
                     os.path.join(ROOT, "tests", "paging_host.cpp"), "-o", out], check=True)
-    L = ctypes.CDLL(out)
-    L.pg_chunk.restype = ctypes.c_longlong
-    L.pg_chunk.argtypes = [ctypes.c_longlong, ctypes.c_int, ctypes.c_int]
-    return L
+    return ctypes.CDLL(out)
 
 
 def test_tiles_and_visibility_match_brute_force(S):
@@ -99,13 +96,18 @@ def test_tiles_and_visibility_match_brute_force(S):
         par = random_trees(1, N, trial)[0]
         cpar = (ctypes.c_int * N)(*par.tolist())
         tiles = (ctypes.c_int * 64)()
-        n_tiles = S.pg_tiles(L, N, page, M, W, sinks, 64, tiles)
+        tile = 64 << trial % 2
+        n_tiles = S.pg_tiles(L, N, page, M, W, sinks, tile, 64, tiles)
         L = min(max(L, 0), cap)
         end = min(L + N, cap)
         read = {x for x in range(end) if S.pg_needs(L, N, page, M, W, sinks, x)}
         got = list(tiles[:n_tiles])
-        assert got == sorted(set(got)) and all(0 <= t * 64 < end for t in got)
-        assert {x // 64 for x in read} <= set(got)
+        assert got == sorted(set(got)) and all(0 <= t * tile < end for t in got)
+        assert {x // tile for x in read} <= set(got)
+        box = S.pg_box(page)
+        assert page % box == 0 and 64 % box == 0
+        for x in range(0, cap, box):
+            assert S.pg_needs_any(L, N, page, M, W, sinks, x, box) == any(y in read for y in range(x, x + box))
         for n in r.choice(N, size=min(N, 6), replace=False):
             chain = streaming.ancestors(par, int(n))
             at = L + len(chain) - 1
@@ -113,6 +115,16 @@ def test_tiles_and_visibility_match_brute_force(S):
             want = {row for row, x in seen if row < end and (W <= 0 or at - x < W or x < sinks)}
             have = {x for x in read if S.pg_sees(int(n), cpar, N, L, x, W, sinks)}
             assert have == want, (L, N, W, sinks, n)
+
+
+def test_division_by_multiplication(S):
+    r = np.random.default_rng(1)
+    top = 2 ** 31 - 1
+    for d in [1, 2, 3, 5, 7, 16, 20, 33, 48, 64, 100, 641, 6700417, 2 ** 30, 2 ** 30 + 1, top] + \
+            [int(x) for x in r.integers(1, top, 50)]:
+        near = [k * d + o for k in (0, 1, 2, top // d // 2, top // d - 1, top // d) for o in (-1, 0, 1)]
+        for n in [x for x in near if 0 <= x <= top] + [top] + [int(x) for x in r.integers(0, top, 40)]:
+            assert S.pg_div(n, d) == n // d, (n, d)
 
 
 def test_rows_and_pieces(S):
@@ -258,6 +270,19 @@ def test_long_sequence_split_over_the_gpu():
     q = torch.randn(B, Hkv * G, N, D, generator=torch.Generator().manual_seed(3)).bfloat16() * 3
     ro, rl = streaming.paged_decode(q, k, v, table, ln, None, None, D ** -0.5)
     o, lse = ga.gpt_attn_paged_decode(*cuda(q, k, v, table, ln))
+    close(o, lse, ro, rl)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scale", [0.0, -0.3, 1e-3, 3.0])
+def test_any_scale(scale):
+    gpu()
+    k, v, table, ln = make_cache(2, 2, 64, 16, [200, 33], 5, seed=1)
+    q = torch.randn(2, 4, 5, 64, generator=torch.Generator().manual_seed(3)).bfloat16()
+    par = random_trees(2, 5, 1)
+    ro, rl = streaming.paged_decode(q, k, v, table, ln, par, None, scale, 100, 2)
+    o, lse = ga.gpt_attn_paged_decode(*cuda(q, k, v, table, ln), scale=scale, window=100, sinks=2,
+                                      parents=torch.as_tensor(par).cuda())
     close(o, lse, ro, rl)
 
 
