@@ -358,48 +358,74 @@ def gpt_attn_bwd_ex(q, k, v, o, lse, dO, scale=None, window=0, head_windows=None
     return dq, dk, dv
 
 
-def _launch(what, device, stream, *args):
+# The calls from here on are often shorter on the GPU than their checks on the host: torch is looked up
+# once, devices are compared by number, and the raw stream is asked for directly.
+_torch = None
+
+
+def _t():
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
+def _launch(what, dev, stream, *args):
     """Calls the entry point `what` with `args` and the stream, the tensors' device being current."""
-    import torch
-    fn = getattr(lib(), what)
-    if device.index == torch.cuda.current_device():
-        rc = fn(*args, _stream_handle(stream))
+    torch = _t()
+    fn = getattr(_lib or lib(), what)
+    if stream is not None:
+        stream = _stream_handle(stream)
+    if dev == torch._C._cuda_getDevice():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream)
     else:
-        with torch.cuda.device(device):
-            rc = fn(*args, _stream_handle(stream))
+        with torch.cuda.device(dev):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream)
     if rc != GPT_ATTN_OK:
         raise GptAttnError(rc, what)
 
 
-def _check_tensor(name, t, dtype, shape, device):
-    """A contiguous CUDA tensor of the given type and shape on `device`."""
-    if t.dtype != dtype or t.device != device or not t.is_cuda or tuple(t.shape) != tuple(shape) or \
-            not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {str(dtype)[6:]} tensor of shape {tuple(shape)} on {device}")
+def _check_tensor(name, t, dtype, shape, dev):
+    """A contiguous tensor of the given type and shape on CUDA device number `dev`."""
+    if t.dtype is not dtype or t.get_device() != dev or dev < 0 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {str(dtype)[6:]} tensor of shape {tuple(shape)} on CUDA device "
+                         f"{dev}")
 
 
-def _check_workspace(t, device):
-    if not t.is_cuda or t.device != device or not t.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+def _check_views(dev, shape, **views):
+    """bf16 tensors of the given [b, h, t, d] shape on CUDA device `dev`, contiguous in their last dimension."""
+    bf16 = _t().bfloat16
+    for n, t in views.items():
+        if t.dtype is not bf16 or t.get_device() != dev or dev < 0 or t.shape != shape or t.stride(3) != 1:
+            raise ValueError(f"{n} must be a bf16 view of shape {tuple(shape)} with stride 1 in its last dimension on "
+                             f"CUDA device {dev}")
 
 
-def _check_sinks_call(q, doc_start, head_windows, lse, views):
-    """The arguments of a call with sinks; returns (B, H, T, D)."""
-    import torch
+def _check_workspace(t, dev):
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on CUDA device {dev}")
+
+
+def _check_sinks_call(q, doc_start, head_windows, lse):
+    """The arguments of a call with sinks; returns (B, H, T, D), the shape and the device number."""
     if q.dim() != 4:
         raise ValueError("q must be a CUDA bf16 [B, H, T, D] view")
-    B, H, T, D = q.shape
-    for n, t in views:
-        _check_view(n, t, q.shape)
-        if t.device != q.device:
-            raise ValueError(f"{n} must be on {q.device}")
+    shape, dev = q.shape, q.get_device()
+    B, H, T, D = shape
     if lse is not None:
-        _check_tensor("lse", lse, torch.float32, (B, H, T), q.device)
+        _check_tensor("lse", lse, _t().float32, (B, H, T), dev)
     if doc_start is not None:
-        _check_tensor("doc_start", doc_start, torch.int32, (B, T), q.device)
+        _check_tensor("doc_start", doc_start, _t().int32, (B, T), dev)
     if head_windows is not None and len(head_windows) != H:
         raise ValueError(f"head_windows needs {H} entries")
-    return B, H, T, D
+    return B, H, T, D, shape, dev
+
+
+def _sinks_mask(H, window, head_windows, doc_start):
+    if head_windows is not None:
+        return _mask(H, window, head_windows, doc_start)
+    return GptAttnMask(int(window), None, None if doc_start is None else doc_start.data_ptr()), None
 
 
 def gpt_attn_fwd_sinks(q, k, v, window=0, sinks=0, scale=None, head_windows=None, doc_start=None, o=None, lse=None,
@@ -407,16 +433,21 @@ def gpt_attn_fwd_sinks(q, k, v, window=0, sinks=0, scale=None, head_windows=None
     """Sliding-window forward in which the first `sinks` tokens of each document (of the row without
     doc_start) stay visible: query i sees key j iff doc_start[i] <= j <= i and (i - j < window or
     j - doc_start[i] < sinks).  Views and the other arguments as for gpt_attn_fwd_ex; returns (o, lse)."""
-    import torch
-    B, H, T, D = _check_sinks_call(q, doc_start, head_windows, lse, (("q", q), ("k", k), ("v", v)))
-    scale = 1.0 / math.sqrt(D) if scale is None else scale
-    o = torch.empty((B, H, T, D), dtype=q.dtype, device=q.device) if o is None else o
-    _check_sinks_call(q, None, None, None, (("o", o),))
-    lse = torch.empty((B, H, T), dtype=torch.float32, device=q.device) if lse is None else lse
-    m, keep = _mask(H, window, head_windows, doc_start)
-    lay = _layout(q=q, k=k, v=v, o=o, dO=o, dq=o, dk=o, dv=o)
-    _launch("gpt_attn_fwd_sinks", q.device, stream, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, H, T, D,
-            float(scale), ctypes.byref(m), int(sinks), _byref(lay))
+    torch = _t()
+    B, H, T, D, shape, dev = _check_sinks_call(q, doc_start, head_windows, lse)
+    _check_views(dev, shape, q=q, k=k, v=v)
+    if o is None:
+        o = torch.empty(shape, dtype=q.dtype, device=q.device)
+    else:
+        _check_views(dev, shape, o=o)
+    if lse is None:
+        lse = torch.empty((B, H, T), dtype=torch.float32, device=q.device)
+    m, keep = _sinks_mask(H, window, head_windows, doc_start)
+    lay = None
+    if not (q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and o.is_contiguous()):
+        lay = _layout(q=q, k=k, v=v, o=o, dO=o, dq=o, dk=o, dv=o)
+    _launch("gpt_attn_fwd_sinks", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), B,
+            H, T, D, D ** -0.5 if scale is None else float(scale), ctypes.byref(m), int(sinks), _byref(lay))
     return o, lse
 
 
@@ -428,25 +459,26 @@ def gpt_attn_bwd_sinks_workspace_bytes(B, H, T, D, window=0, sinks=0) -> int:
 def gpt_attn_bwd_sinks(q, k, v, o, lse, dO, window=0, sinks=0, scale=None, head_windows=None, doc_start=None,
                        dq=None, dk=None, dv=None, workspace=None, stream=None):
     """Backward pass of gpt_attn_fwd_sinks under the same mask; returns (dq, dk, dv)."""
-    import torch
-    B, H, T, D = _check_sinks_call(q, doc_start, head_windows, lse,
-                                   (("q", q), ("k", k), ("v", v), ("o", o), ("dO", dO)))
-    scale = 1.0 / math.sqrt(D) if scale is None else scale
-    mk = lambda: torch.empty((B, H, T, D), dtype=q.dtype, device=q.device)
-    dq = mk() if dq is None else dq
-    dk = mk() if dk is None else dk
-    dv = mk() if dv is None else dv
-    _check_sinks_call(q, None, None, None, (("dq", dq), ("dk", dk), ("dv", dv)))
+    torch = _t()
+    B, H, T, D, shape, dev = _check_sinks_call(q, doc_start, head_windows, lse)
+    _check_views(dev, shape, q=q, k=k, v=v, o=o, dO=dO)
+    dtype, device = q.dtype, q.device
+    dq = torch.empty(shape, dtype=dtype, device=device) if dq is None else dq
+    dk = torch.empty(shape, dtype=dtype, device=device) if dk is None else dk
+    dv = torch.empty(shape, dtype=dtype, device=device) if dv is None else dv
+    _check_views(dev, shape, dq=dq, dk=dk, dv=dv)
     if workspace is None:
         top = max(head_windows) if head_windows is not None else window
         workspace = torch.empty(max(gpt_attn_bwd_sinks_workspace_bytes(B, H, T, D, top, sinks), 16),
-                                dtype=torch.uint8, device=q.device)
-    _check_workspace(workspace, q.device)
-    m, keep = _mask(H, window, head_windows, doc_start)
+                                dtype=torch.uint8, device=device)
+    else:
+        _check_workspace(workspace, dev)
+    m, keep = _sinks_mask(H, window, head_windows, doc_start)
     lay = _layout(q=q, k=k, v=v, o=o, dO=dO, dq=dq, dk=dk, dv=dv)
-    _launch("gpt_attn_bwd_sinks", q.device, stream, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dO),
-            _ptr(dq), _ptr(dk), _ptr(dv), B, H, T, D, float(scale), ctypes.byref(m), int(sinks), _byref(lay),
-            _ptr(workspace), workspace.numel() * workspace.element_size())
+    _launch("gpt_attn_bwd_sinks", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
+            dO.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, H, T, D,
+            D ** -0.5 if scale is None else float(scale), ctypes.byref(m), int(sinks), _byref(lay), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size())
     return dq, dk, dv
 
 
@@ -523,34 +555,30 @@ def gpt_attn_decode(q, k_cache, v_cache, seq_lens, scale=None, window=0, o=None,
     return o, lse
 
 
-def _check_int32(name, t, shape, device):
-    import torch
-    if t.dtype != torch.int32 or t.device != device or not t.is_cuda or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)} on {device}")
+def _check_int32(name, t, shape, dev):
+    _check_tensor(name, t, _t().int32, shape, dev)
 
 
 def _check_pools(k_pages, v_pages):
-    import torch
-    if k_pages.dim() != 4 or not k_pages.is_cuda:
+    """Two pools [n_pages, Hkv, page, D]; returns their shape and device number."""
+    shape, dev, bf16 = k_pages.shape, k_pages.get_device(), _t().bfloat16
+    if len(shape) != 4 or dev < 0:
         raise ValueError("k_pages must be a contiguous CUDA bf16 tensor [n_pages, Hkv, page, D]")
-    for n, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        if t.dtype != torch.bfloat16 or t.device != k_pages.device or t.shape != k_pages.shape or \
-                not t.is_contiguous():
-            raise ValueError(f"{n} must be a contiguous bf16 tensor of shape {tuple(k_pages.shape)} on "
-                             f"{k_pages.device}")
+    _check_tensor("k_pages", k_pages, bf16, shape, dev)
+    _check_tensor("v_pages", v_pages, bf16, shape, dev)
+    return shape, dev
 
 
 def _paged_cache(k_pages, v_pages, table, lens):
-    """A GptAttnPagedCache of the checked tensors."""
-    _check_pools(k_pages, v_pages)
+    """A GptAttnPagedCache of the checked tensors, and the device number."""
+    (P, Hkv, page, D), dev = _check_pools(k_pages, v_pages)
     if table.dim() != 2:
         raise ValueError("table must be a contiguous int32 tensor [B, max_pages]")
-    _check_int32("table", table, table.shape, k_pages.device)
     B, M = table.shape
-    _check_int32("lens", lens, (B,), k_pages.device)
-    P, Hkv, page, D = k_pages.shape
+    _check_int32("table", table, (B, M), dev)
+    _check_int32("lens", lens, (B,), dev)
     return GptAttnPagedCache(k_pages.data_ptr(), v_pages.data_ptr(), table.data_ptr(), lens.data_ptr(), B, Hkv, D, P,
-                             page, M)
+                             page, M), dev
 
 
 def _pair_strides(a, b):
@@ -565,15 +593,12 @@ def _pair_strides(a, b):
 def gpt_attn_paged_append(k_pages, v_pages, table, lens, k_new, v_new, n_new=None, stream=None):
     """Writes the rows of N new tokens (k_new, v_new: bf16 [B, Hkv, N, D] views) of every sequence into
     its pages, token n at position lens[b] + n; n_new (int32 [B]): how many of them are used."""
-    cache = _paged_cache(k_pages, v_pages, table, lens)
+    cache, dev = _paged_cache(k_pages, v_pages, table, lens)
     N = k_new.shape[2] if k_new.dim() == 4 else 0
-    for n, t in (("k_new", k_new), ("v_new", v_new)):
-        _check_view(n, t, (cache.B, cache.Hkv, N, cache.D))
-        if t.device != k_pages.device:
-            raise ValueError(f"{n} must be on {k_pages.device}")
+    _check_views(dev, (cache.B, cache.Hkv, N, cache.D), k_new=k_new, v_new=v_new)
     if n_new is not None:
-        _check_int32("n_new", n_new, (cache.B,), k_pages.device)
-    _launch("gpt_attn_paged_append", k_pages.device, stream, ctypes.byref(cache), _ptr(k_new), _ptr(v_new), N,
+        _check_int32("n_new", n_new, (cache.B,), dev)
+    _launch("gpt_attn_paged_append", dev, stream, ctypes.byref(cache), k_new.data_ptr(), v_new.data_ptr(), N,
             _ptr(n_new), _pair_strides(k_new, v_new))
 
 
@@ -587,49 +612,47 @@ def gpt_attn_paged_decode(q, k_pages, v_pages, table, lens, parents=None, n_new=
     already appended) over the paged cache and, by the tree `parents` (int32 [B, N]; None: one after the
     other), over each other.  With a window each sees the tokens within it and the first `sinks` ones.
     Returns (o [B, H, N, D], lse [B, H, N])."""
-    import torch
-    cache = _paged_cache(k_pages, v_pages, table, lens)
+    torch = _t()
+    cache, dev = _paged_cache(k_pages, v_pages, table, lens)
     if q.dim() != 4:
         raise ValueError("q must be a CUDA bf16 [B, H, N, D] view")
-    B, H, N, D = q.shape
-    device = k_pages.device
-    _check_view("q", q, (cache.B, H, N, cache.D))
+    shape, device = q.shape, q.device
+    _, H, N, D = shape
+    B = cache.B
+    _check_views(dev, (B, H, N, cache.D), q=q)
     if o is None:
-        o = torch.empty((B, H, N, D), dtype=q.dtype, device=device)
+        o = torch.empty(shape, dtype=q.dtype, device=device)
     else:
-        _check_view("o", o, q.shape)
-    if q.device != device or o.device != device:
-        raise ValueError(f"q and o must be on {device}")
+        _check_views(dev, shape, o=o)
     if lse is None:
         lse = torch.empty((B, H, N), dtype=torch.float32, device=device)
     else:
-        _check_tensor("lse", lse, torch.float32, (B, H, N), device)
+        _check_tensor("lse", lse, torch.float32, (B, H, N), dev)
     if parents is not None:
-        _check_int32("parents", parents, (B, N), device)
+        _check_int32("parents", parents, (B, N), dev)
     if n_new is not None:
-        _check_int32("n_new", n_new, (B,), device)
+        _check_int32("n_new", n_new, (B,), dev)
     if workspace is None:
         need = gpt_attn_paged_decode_workspace_bytes(B, H, cache.Hkv, N, D)
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
     else:
-        _check_workspace(workspace, device)
-    scale = 1.0 / math.sqrt(D) if scale is None else scale
-    _launch("gpt_attn_paged_decode", device, stream, _ptr(q), ctypes.byref(cache), _ptr(n_new), _ptr(parents), _ptr(o),
-            _ptr(lse), H, N, float(scale), int(window), int(sinks), _pair_strides(q, o), _ptr(workspace),
-            workspace.numel() * workspace.element_size())
+        _check_workspace(workspace, dev)
+    _launch("gpt_attn_paged_decode", dev, stream, q.data_ptr(), ctypes.byref(cache), _ptr(n_new), _ptr(parents),
+            o.data_ptr(), lse.data_ptr(), H, N, D ** -0.5 if scale is None else float(scale), int(window), int(sinks),
+            _pair_strides(q, o), workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return o, lse
 
 
 def gpt_attn_paged_accept(k_pages, v_pages, table, lens, accepted, n_accepted, stream=None):
     """Moves the rows of the accepted nodes up: node accepted[b, i] (int32 [B, N]) to position
     lens[b] + i for i < n_accepted[b] (int32 [B]).  lens itself is the caller's to change."""
-    cache = _paged_cache(k_pages, v_pages, table, lens)
+    cache, dev = _paged_cache(k_pages, v_pages, table, lens)
     if accepted.dim() != 2:
         raise ValueError("accepted must be a contiguous int32 tensor [B, N]")
-    _check_int32("accepted", accepted, (cache.B, accepted.shape[1]), k_pages.device)
-    _check_int32("n_accepted", n_accepted, (cache.B,), k_pages.device)
-    _launch("gpt_attn_paged_accept", k_pages.device, stream, ctypes.byref(cache), _ptr(accepted), _ptr(n_accepted),
-            accepted.shape[1])
+    N = accepted.shape[1]
+    _check_int32("accepted", accepted, (cache.B, N), dev)
+    _check_int32("n_accepted", n_accepted, (cache.B,), dev)
+    _launch("gpt_attn_paged_accept", dev, stream, ctypes.byref(cache), accepted.data_ptr(), n_accepted.data_ptr(), N)
 
 
 def gpt_attn_pages_workspace_bytes(S, M, P) -> int:
@@ -637,38 +660,43 @@ def gpt_attn_pages_workspace_bytes(S, M, P) -> int:
 
 
 def _check_state(table, refs, lens=None):
-    """Table, lengths and holders of the pages; returns (S, M, P, device)."""
+    """Table, lengths and holders of the pages; returns (S, M, P, device number)."""
     if table.dim() != 2 or refs.dim() != 1:
         raise ValueError("table must be an int32 tensor [S, M] and refs one [P]")
-    _check_int32("table", table, table.shape, table.device)
-    _check_int32("refs", refs, refs.shape, table.device)
+    S, M = table.shape
+    P, dev = refs.shape[0], table.get_device()
+    _check_int32("table", table, (S, M), dev)
+    _check_int32("refs", refs, (P,), dev)
     if lens is not None:
-        _check_int32("lens", lens, table.shape[:1], table.device)
-    return (*table.shape, refs.shape[0], table.device)
+        _check_int32("lens", lens, (S,), dev)
+    return S, M, P, dev
 
 
-def _pages_workspace(workspace, S, M, P, device):
-    import torch
+def _pages_workspace(workspace, S, M, P, table):
     if workspace is None:
-        return torch.empty(max(gpt_attn_pages_workspace_bytes(S, M, P), 16), dtype=torch.uint8, device=device)
-    _check_workspace(workspace, device)
+        return _t().empty(max(gpt_attn_pages_workspace_bytes(S, M, P), 16), dtype=_t().uint8, device=table.device)
+    _check_workspace(workspace, table.get_device())
     return workspace
+
+
+def _int32_out(name, t, shape, like):
+    """An int32 result of the given shape: the caller's, checked, or a new one on the device of `like`."""
+    if t is None:
+        return _t().empty(shape, dtype=_t().int32, device=like.device)
+    _check_int32(name, t, shape, like.get_device())
+    return t
 
 
 def gpt_attn_pages_reserve(table, lens, refs, page, tokens, status=None, workspace=None, stream=None):
     """Gives every slot pages for tokens[s] (int32 [S]) more tokens, the lowest free ones first; table
     and refs change in place.  Returns status int32 [S]: 0 nothing asked, 1 done, -1 refused (the table's
     row is too short), -2 not enough free pages."""
-    import torch
-    S, M, P, device = _check_state(table, refs, lens)
-    _check_int32("tokens", tokens, (S,), device)
-    if status is None:
-        status = torch.empty(S, dtype=torch.int32, device=device)
-    else:
-        _check_int32("status", status, (S,), device)
-    ws = _pages_workspace(workspace, S, M, P, device)
-    _launch("gpt_attn_pages_reserve", device, stream, _ptr(table), _ptr(lens), _ptr(refs), S, M, P, int(page),
-            _ptr(tokens), _ptr(status), _ptr(ws), ws.numel() * ws.element_size())
+    S, M, P, dev = _check_state(table, refs, lens)
+    _check_int32("tokens", tokens, (S,), dev)
+    status = _int32_out("status", status, (S,), table)
+    ws = _pages_workspace(workspace, S, M, P, table)
+    _launch("gpt_attn_pages_reserve", dev, stream, table.data_ptr(), lens.data_ptr(), refs.data_ptr(), S, M, P, int(page),
+            tokens.data_ptr(), status.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
     return status
 
 
@@ -677,56 +705,48 @@ def gpt_attn_pages_fork(table, lens, refs, page, parents, status=None, pairs=Non
     shared, a partial last page gets a page of its own.  Table, lens and refs change in place.  Returns
     (status int32 [S], pairs int32 [S, 2]): status as for gpt_attn_pages_reserve, pairs the pages to copy
     with gpt_attn_pages_copy in every layer's pools."""
-    import torch
-    S, M, P, device = _check_state(table, refs, lens)
-    _check_int32("parents", parents, (S,), device)
-    if status is None:
-        status = torch.empty(S, dtype=torch.int32, device=device)
-    else:
-        _check_int32("status", status, (S,), device)
-    if pairs is None:
-        pairs = torch.empty((S, 2), dtype=torch.int32, device=device)
-    else:
-        _check_int32("pairs", pairs, (S, 2), device)
-    ws = _pages_workspace(workspace, S, M, P, device)
-    _launch("gpt_attn_pages_fork", device, stream, _ptr(table), _ptr(lens), _ptr(refs), S, M, P, int(page),
-            _ptr(parents), _ptr(status), _ptr(pairs), _ptr(ws), ws.numel() * ws.element_size())
+    S, M, P, dev = _check_state(table, refs, lens)
+    _check_int32("parents", parents, (S,), dev)
+    status = _int32_out("status", status, (S,), table)
+    pairs = _int32_out("pairs", pairs, (S, 2), table)
+    ws = _pages_workspace(workspace, S, M, P, table)
+    _launch("gpt_attn_pages_fork", dev, stream, table.data_ptr(), lens.data_ptr(), refs.data_ptr(), S, M, P, int(page),
+            parents.data_ptr(), status.data_ptr(), pairs.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
     return status, pairs
 
 
 def gpt_attn_pages_free(table, lens, refs, drop, stream=None):
     """Slots with drop[s] > 0 (int32 [S]) give their pages back; table, lens and refs change in place."""
-    S, M, P, device = _check_state(table, refs, lens)
-    _check_int32("drop", drop, (S,), device)
-    _launch("gpt_attn_pages_free", device, stream, _ptr(table), _ptr(lens), _ptr(refs), S, M, P, _ptr(drop))
+    S, M, P, dev = _check_state(table, refs, lens)
+    _check_int32("drop", drop, (S,), dev)
+    _launch("gpt_attn_pages_free", dev, stream, table.data_ptr(), lens.data_ptr(), refs.data_ptr(), S, M, P, drop.data_ptr())
 
 
 def gpt_attn_pages_compact(table, refs, workspace=None, stream=None):
     """Packs the n pages in use into places 0 to n - 1.  Returns (new_table, new_refs, pairs int32
     [P // 2, 2], moves int32 [1]); gpt_attn_pages_copy(k, v, pairs, n_pairs=moves) moves the pages."""
-    import torch
-    S, M, P, device = _check_state(table, refs)
-    new_table, new_refs = torch.empty_like(table), torch.empty_like(refs)
-    pairs = torch.empty((P // 2, 2), dtype=torch.int32, device=device)
-    moves = torch.empty(1, dtype=torch.int32, device=device)
-    ws = _pages_workspace(workspace, S, M, P, device)
-    _launch("gpt_attn_pages_compact", device, stream, _ptr(table), _ptr(refs), S, M, P, _ptr(new_table),
-            _ptr(new_refs), _ptr(pairs), _ptr(moves), _ptr(ws), ws.numel() * ws.element_size())
+    S, M, P, dev = _check_state(table, refs)
+    new_table, new_refs = _t().empty_like(table), _t().empty_like(refs)
+    pairs = _int32_out("pairs", None, (P // 2, 2), table)
+    moves = _int32_out("moves", None, (1,), table)
+    ws = _pages_workspace(workspace, S, M, P, table)
+    _launch("gpt_attn_pages_compact", dev, stream, table.data_ptr(), refs.data_ptr(), S, M, P, new_table.data_ptr(),
+            new_refs.data_ptr(), pairs.data_ptr(), moves.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
     return new_table, new_refs, pairs, moves
 
 
 def gpt_attn_pages_copy(k_pages, v_pages, pairs, n_pairs=None, stream=None):
     """Copies page pairs[i, 0] onto page pairs[i, 1] in both pools, for the first n_pairs (int32 [1] on
     the device; None: all) rows of pairs (int32 [n, 2]); rows with a page outside the pools are skipped."""
-    _check_pools(k_pages, v_pages)
+    (P, Hkv, page, D), dev = _check_pools(k_pages, v_pages)
     if pairs.dim() != 2:
         raise ValueError("pairs must be a contiguous int32 tensor [n, 2]")
-    _check_int32("pairs", pairs, (pairs.shape[0], 2), k_pages.device)
+    n = pairs.shape[0]
+    _check_int32("pairs", pairs, (n, 2), dev)
     if n_pairs is not None:
-        _check_int32("n_pairs", n_pairs, (1,), k_pages.device)
-    P, Hkv, page, D = k_pages.shape
-    _launch("gpt_attn_pages_copy", k_pages.device, stream, _ptr(k_pages), _ptr(v_pages), P, Hkv, page, D, _ptr(pairs),
-            pairs.shape[0], _ptr(n_pairs))
+        _check_int32("n_pairs", n_pairs, (1,), dev)
+    _launch("gpt_attn_pages_copy", dev, stream, k_pages.data_ptr(), v_pages.data_ptr(), P, Hkv, page, D,
+            pairs.data_ptr(), n, _ptr(n_pairs))
 
 
 def gpt_attn_qk_prologue_fwd(q_raw, k_raw, qk_norm=True, rope_base=10000.0, q_out=None, k_out=None, stream=None):
