@@ -177,6 +177,24 @@ bool set_smem(Kern k, size_t bytes) {
     return true;
 }
 
+// Launches a kernel that may start before the one before it in the stream has ended (it waits for
+// that itself, see sm100.cuh).
+template <typename... Params, typename... Args>
+bool launch_dependent(void (*kernel)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st,
+                      const Args&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess && cudaGetLastError() == cudaSuccess;
+}
+
 int sm_count();
 
 // Kernel-side mask parameters from the C ABI's description (nullptr: plain causal).  Per-head
@@ -572,18 +590,11 @@ int launch_paged(const PagedParams& p, int grid, cudaStream_t st) {
         !set_smem(paged_decode_kernel<D, MT>, smem))
         return GPT_ATTN_ERR_CUDA;
     paged_decode_kernel<D, MT><<<grid, kPagedThreads, smem, st>>>(mk, mv, p);
+    if (cudaGetLastError() != cudaSuccess) return GPT_ATTN_ERR_CUDA;
     const int item_rows = p.R < 16 * MT ? p.R : 16 * MT;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(p.B * p.Hkv * p.RB), (unsigned)((item_rows + kCombineWarps - 1) / kCombineWarps));
-    cfg.blockDim = dim3(32 * kCombineWarps);
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, paged_combine_kernel<D, MT>, p) != cudaSuccess) return GPT_ATTN_ERR_CUDA;
-    return cudaGetLastError() == cudaSuccess ? GPT_ATTN_OK : GPT_ATTN_ERR_CUDA;
+    const dim3 cgrid((unsigned)(p.B * p.Hkv * p.RB), (unsigned)((item_rows + kCombineWarps - 1) / kCombineWarps));
+    return launch_dependent(paged_combine_kernel<D, MT>, cgrid, 32 * kCombineWarps, 0, st, p) ? GPT_ATTN_OK
+                                                                                              : GPT_ATTN_ERR_CUDA;
 }
 
 template <int D>
@@ -868,9 +879,9 @@ int gpt_attn_paged_decode(const void* q, const gpt_attn_paged_cache* cache, cons
     p.q_keep = scale == 0.f ? 0u : 0xffffffffu;
     p.q_flip = scale < 0.f ? 0x80008000u : 0u;
     p.timeout_ns = wait_timeout_ns();
-    // No more blocks than the tables can name tiles, the number of which has to fit an int.
+    // No more blocks than the tables can name tiles; places in the list of them have to fit an int.
     const int tile = D == 64 ? PagedCfg<64>::kTile : PagedCfg<128>::kTile;
-    const long long items = (long long)B * c.Hkv * s.RB, tiles = (c.cap + tile - 1) / tile;
+    const long long items = (long long)B * c.Hkv * s.RB, tiles = (c.cap + tile - 1) / tile + kPagedItemCost;
     if (items > 0x7fffffffLL / tiles) return GPT_ATTN_ERR_SHAPE;
     const long long most = items * tiles;
     const int grid = (int)(most < kPagedBlocks ? most : kPagedBlocks);

@@ -11,9 +11,9 @@
 //     lets them be (the largest power of two that divides it, so a tile takes 8 boxes from pages of 16
 //     tokens, 128 from odd pages), one lane to a box.  Boxes that nobody sees and missing pages are
 //     not read but zero-filled.  A tile's pages are looked up while the tile before it is issued.
-//   - All tiles of all (sequence, key head, row block) items form one list, cut into equal pieces,
-//     one to a team of warps (two teams to an SM): ragged batches and single long sequences fill the
-//     GPU alike.  The ring runs on across items.  A piece that holds a whole item writes O and lse;
+//   - All (sequence, key head, row block) items form one list, each as long as its tiles and what it
+//     costs besides, cut into equal pieces, one to a team of warps (two teams to an SM): ragged batches
+//     and single long sequences fill the GPU alike.  The ring runs on across items.  A piece that holds a whole item writes O and lse;
 //     the others leave fp32 partial results, joined by paged_combine_kernel.
 //   - Four warps of a team compute: scores and P V on warp-level matrix instructions (16 rows x 16 keys
 //     a step; a tcgen05 tile has 128 rows, of which a call has 1 to 64), the softmax in registers
@@ -37,7 +37,9 @@ constexpr int kPagedTeams = 2;                                // of a block
 constexpr int kPagedTeamWarps = 4;
 constexpr int kPagedTeam = 32 * kPagedTeamWarps;
 constexpr int kPagedThreads = kPagedTeams * kPagedTeam + 128; // and a warpgroup with a producer warp for each team
-constexpr int kPagedLeastTiles = 1;      // tiles of a piece at least
+// What an item costs besides its tiles (its rows in, its states joined, its output), in tiles.  Pieces
+// are cut by tiles and items together: cut by tiles alone, those with an item's end in them ran on, %COST.
+constexpr int kPagedItemCost = 1;
 // Registers of a thread: 168 at the launch, given up by the producers' warpgroup and taken by the teams.
 constexpr int kPagedProducerRegs = 88, kPagedTeamRegs = 208;
 
@@ -54,7 +56,7 @@ struct PagedParams {
     Strides q_str, o_str;         // [b, h, n, d]
     float* part_o;                // [2 * teams, rows of a row block, D]
     float* part_ml;               // [2 * teams, rows of a row block, 2]
-    int* prefix;                  // [B + 1] first tile of each sequence in the list, then chunk
+    int* prefix;                  // [B + 1] place of each sequence in the list, then the pieces' length
     int B, H, Hkv, G, N;
     FastDiv by_n;                 // N
     int R, RB;                    // rows of an item, row blocks
@@ -116,16 +118,40 @@ __device__ __forceinline__ uint32_t paged_at(int r, int c) {
     return (c >> 3) * (PagedCfg<D>::kTile * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
-// A place in the list: tile t of item (sequence b, key head h, row block rb).
+// A place in the list: tile t of item (sequence b, key head h, row block rb), number `pos` of the list.
 struct PagedAt {
-    int b, h, rb, t;
+    int b, h, rb, t, pos;
 };
+
+// Length of an item of the list.
+__device__ __forceinline__ int paged_item(int n_tiles) { return n_tiles + kPagedItemCost; }
+
+// On to the next tile; false (and nowhere) at the end of the piece.
+__device__ __forceinline__ bool paged_step(const PagedParams& p, PagedAt& at, PagedSpan& sp, int tile, int end) {
+    ++at.pos;
+    if (at.t + 1 == sp.n_tiles) {
+        at.pos += kPagedItemCost;
+        if (at.pos >= end) return false;
+        at.t = 0;
+        if (++at.rb == p.RB) {
+            at.rb = 0;
+            if (++at.h == p.Hkv) {
+                at.h = 0;
+                do sp = paged_seq_span(p, ++at.b, tile);
+                while (sp.n_tiles == 0);
+            }
+        }
+        return true;
+    }
+    ++at.t;
+    return at.pos < end;
+}
 
 // What the computing warps have to know of one tile.
 struct PagedTile {
     uint32_t seen[4];             // keys of the tile that some row may see
     int key0;                     // its first key
-    int mask;                     // some row may not see some of them
+    int mask;                     // some row may not see some key of the tile
 };
 
 // One team's shared memory.
@@ -153,12 +179,12 @@ struct PagedSmem {
 };
 
 // One of the two producer warps of a team, for its keys (which = 0) or values (1): walks the team's
-// piece of n_mine tiles, one tile a step.  Such a warp issues nearly alone, at 6 to 8 cycles an
+// piece of the list, up to place `end`, one tile a step.  Such a warp issues nearly alone, at 6 to 8 cycles an
 // instruction and some 80 a load, so instructions count here: one warp for both, with integer
 // divisions and the table's entries awaited where they were looked up, bounded the kernel.
 template <int D>
 __device__ __forceinline__ void paged_produce(const PagedParams& p, const CUtensorMap* tm, PagedTeam<D>& sm, int which,
-                                              int n_mine, const AbortCtl& ac) {
+                                              int end, const AbortCtl& ac) {
     using C = PagedCfg<D>;
     constexpr int kTile = C::kTile, kWords = C::kWords, kStages = C::kStages;
     const int lane = threadIdx.x & 31;
@@ -186,7 +212,7 @@ __device__ __forceinline__ void paged_produce(const PagedParams& p, const CUtens
     }
     int i = 0, s = -1;
     uint32_t lap = 0;                                // parity of the stage's last release
-    for (; i < n_mine; ++i) {
+    for (bool more = true; more; ++i) {
         if (++s == kStages) {
             s = 0;
             lap ^= 1;
@@ -211,6 +237,7 @@ __device__ __forceinline__ void paged_produce(const PagedParams& p, const CUtens
             }
 #pragma unroll
             for (int w = 0; w < kWords; ++w) d.seen[w] = 0xffffffffu;
+            d.mask |= !all;
             if (!all) {
 #pragma unroll
                 for (int w = 0; w < kWords; ++w) {
@@ -224,19 +251,10 @@ __device__ __forceinline__ void paged_produce(const PagedParams& p, const CUtens
             }
         }
         // the next tile's pages
-        if (i + 1 < n_mine) {
-            if (++at.t == sp.n_tiles) {
-                at.t = 0;
-                if (++at.rb == p.RB) {
-                    at.rb = 0;
-                    if (++at.h == p.Hkv) {
-                        at.h = 0;
-                        do sp = paged_seq_span(p, ++at.b, kTile);
-                        while (sp.n_tiles == 0);
-                        table = p.table + (size_t)at.b * p.max_pages;
-                    }
-                }
-            }
+        const int b = at.b;
+        more = paged_step(p, at, sp, kTile, end);
+        if (more) {
+            if (at.b != b) table = p.table + (size_t)at.b * p.max_pages;
             h = at.h;
 #pragma unroll
             for (int w = 0; w < kWords; ++w)
@@ -278,8 +296,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     extern __shared__ uint8_t smem_raw[];
     PagedSmem<D>& block = *reinterpret_cast<PagedSmem<D>*>(smem_align1024(smem_raw));
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    asm volatile("griddepcontrol.launch_dependents;");
-
+    launch_dependents();
     if (threadIdx.x == 0) {
         for (int g = 0; g < kPagedTeams; ++g) {
             for (int s = 0; s < kStages; ++s) {
@@ -304,10 +321,11 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 
     // ---- the teams' pieces of the list.  Team g of block x is number g * blocks + x, so that short
     // lists take an SM a piece.
-    int total = 0, mine = 0, upto = 0;               // tiles of all sequences; of sequence b, and up to its end
+    int total = 0, mine = 0, upto = 0;               // lengths of all sequences; of sequence b, and up to its end
     auto count = [&](int base) {
         const int b = base + threadIdx.x;
-        mine = upto = b < p.B ? paged_seq_span(p, b, kTile).n_tiles * p.Hkv * p.RB : 0;
+        const int n_tiles = b < p.B ? paged_seq_span(p, b, kTile).n_tiles : 0;
+        mine = upto = n_tiles > 0 ? paged_item(n_tiles) * p.Hkv * p.RB : 0;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, upto, off);
@@ -325,16 +343,17 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         }
     };
     for (int base = 0; base < p.B; base += kPagedThreads) count(base);
-    const int chunk = paged_chunk(total, kPagedTeams * gridDim.x, kPagedLeastTiles), all = total;
+    const int chunk = paged_chunk(total, kPagedTeams * gridDim.x, 1), all = total;
     auto find = [&](int base) {
         const int b = base + threadIdx.x;
         if (b >= p.B) return;
         for (int g = 0; g < kPagedTeams; ++g) {
             const long long begin = (long long)chunk * (g * gridDim.x + blockIdx.x);
             if (begin >= upto - mine && begin < upto) {
-                const int n_tiles = paged_seq_span(p, b, kTile).n_tiles;
-                const int in_b = (int)begin - (upto - mine), x = in_b / n_tiles;
-                block.team[g].start = PagedAt{b, x / p.RB, x % p.RB, in_b - x * n_tiles};
+                const int len = paged_item(paged_seq_span(p, b, kTile).n_tiles), in_b = (int)begin - (upto - mine);
+                const int x = in_b / len, in_x = in_b - x * len;              // the item, and the place in it
+                block.team[g].start = PagedAt{b, x / p.RB, x % p.RB, max(in_x - kPagedItemCost, 0),
+                                              (int)begin + max(kPagedItemCost - in_x, 0)};
             }
         }
         if (blockIdx.x == 0) p.prefix[b] = upto - mine;
@@ -359,15 +378,16 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     const int extra = warp - kPagedTeams * kPagedTeamWarps;
     const int g = extra < 0 ? warp / kPagedTeamWarps : extra / 2;
     const int team_no = g * gridDim.x + blockIdx.x;
-    const int n_mine = (int)max(0ll, min((long long)chunk, all - (long long)chunk * team_no));
+    const int end = (int)min((long long)all, (long long)chunk * (team_no + 1));
+    const bool none = (long long)chunk * team_no >= all || block.team[g].start.pos >= end;
     const AbortCtl ac{&block.abort, p.timeout_ns};
     if (extra >= 0) {
         regs_dec<kPagedProducerRegs>();
-        if (n_mine > 0) paged_produce<D>(p, extra & 1 ? &tm_v : &tm_k, block.team[g], extra & 1, n_mine, ac);
+        if (!none) paged_produce<D>(p, extra & 1 ? &tm_v : &tm_k, block.team[g], extra & 1, end, ac);
         return;
     }
     regs_inc<kPagedTeamRegs>();
-    if (n_mine == 0) return;
+    if (none) return;
     PagedTeam<D>& sm = block.team[g];
     const int tid = threadIdx.x - g * kPagedTeam, w4 = warp - g * kPagedTeamWarps;
 
@@ -492,7 +512,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     };
     if (!set_up()) return;
 
-    for (int i = 0; i < n_mine; ++i) {
+    bool more = true;
+    for (int i = 0; more; ++i) {
         if (++s == kStages) s = 0;
         if (s == 0) lap ^= 1;
         if (!warp_wait(&sm.bar_full[s], lap, ac)) return;
@@ -523,21 +544,19 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         // keys behind the cached tokens, at a window's edge or on missing pages; rows of nodes that
         // do not exist see nothing anywhere, which the end of the item takes care of
         const int mask = t.mask;
-        uint32_t seen[(kKeys + 31) / 32];            // of the warp's keys
-        bool full = true;
-#pragma unroll
-        for (int w = 0; w < (kKeys + 31) / 32; ++w) {
-            seen[w] = t.seen[kb / 32 + w] >> (kb & 31);
-            full = full && (kKeys < 32 ? (~seen[w] & ((1u << (kKeys & 31)) - 1)) == 0 : seen[w] == 0xffffffffu);
-        }
-        if (mask || !full) {
+        // one token, and keys of each warp's own: a warp goes by its own keys alone
+        constexpr bool kOwnKeys = KS == kPagedTeamWarps;
+        bool partial = mask;
+        if (kOwnKeys && p.N == 1) partial = mask && (~(t.seen[kb / 32] >> (kb & 31)) & bits_below(kKeys)) != 0;
+        if (partial) {
             const int key0 = t.key0 + kb;
 #pragma unroll
             for (int e = 0; e < 2; ++e)
 #pragma unroll
                 for (int w = 0; w < (NT + 3) / 4; ++w) {
                     // this lane's keys of the word: bits 0 and 1, 8 and 9, ...
-                    const uint32_t see = (seen[w] & paged_sees(key0 + w * 32, sp.L, lower[e], p.sinks, vis[e])) >>
+                    const uint32_t see = ((t.seen[kb / 32 + w] >> (kb & 31)) &
+                                          paged_sees(key0 + w * 32, sp.L, lower[e], p.sinks, vis[e])) >>
                                          ((lane & 3) * 2);
 #pragma unroll
                     for (int n = 0; n < 4 && w * 4 + n < NT; ++n)
@@ -585,28 +604,31 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             pf[n / 2][(n & 1) * 2] = pack_bf16x2(p0, p1);
             pf[n / 2][(n & 1) * 2 + 1] = pack_bf16x2(p2, p3);
         }
-        // Rows that came along in a box without being seen may hold anything: their values are cleared,
-        // by every warp for itself.
-        if (!full) {
-            for (int c = lane; c < kKeys * kChunks; c += 32) {
-                const int key = c / kChunks;
-                if (!((t.seen[(kb + key) >> 5] >> ((kb + key) & 31)) & 1))
-                    *reinterpret_cast<uint4*>(vt + paged_at<D>(kb + key, c % kChunks)) = make_uint4(0u, 0u, 0u, 0u);
+        // Rows that came along in a box without being seen may hold anything, and new tokens that are not
+        // every node's ancestors infinities and NaN, which must not reach the others through 0 * NaN.
+        // The former are cleared; where there are some of the latter, they are added to the rows with
+        // P > 0 one by one and then cleared as well.
+        if (kOwnKeys && p.N == 1) {
+            // only the former
+#pragma unroll 1
+            for (int c = partial ? lane : kKeys * kChunks; c < kKeys * kChunks; c += 32) {
+                const int key = kb + c / kChunks;
+                if (!((t.seen[key >> 5] >> (key & 31)) & 1))
+                    *reinterpret_cast<uint4*>(vt + paged_at<D>(key, c % kChunks)) = make_uint4(0u, 0u, 0u, 0u);
             }
             __syncwarp();
-        }
-        // New tokens that are not every node's ancestors may hold infinities or NaN, which must not
-        // reach the others through 0 * NaN.  Where a tile holds some, they are added to the rows with
-        // P > 0 one by one and then cleared in the stage.
-        if (mask && p.N > 1) {
+        } else if (mask) {
             uint4* rows = reinterpret_cast<uint4*>(vt);
             bool odd = false;
-#pragma unroll 4
+#pragma unroll 2
             for (int c = tid; c < kTile * kChunks; c += kPagedTeam) {
                 const int key = (c >> 3) & (kTile - 1);
-                const uint4 x = rows[c];
-                if ((t.seen[key >> 5] >> (key & 31)) & 1)
+                if (!((t.seen[key >> 5] >> (key & 31)) & 1)) {
+                    rows[c] = make_uint4(0u, 0u, 0u, 0u);
+                } else if (p.N > 1) {
+                    const uint4 x = rows[c];
                     odd = odd || not_finite(x.x) || not_finite(x.y) || not_finite(x.z) || not_finite(x.w);
+                }
             }
             odd = __any_sync(0xffffffffu, odd);
             int(&any)[kPagedTeamWarps] = sm.odd[joins & 1];       // a warp may be a join ahead of the readers
@@ -665,7 +687,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         }
 
         const bool done = at.t == sp.n_tiles - 1;
-        if (done || i == n_mine - 1) {
+        if (done || at.pos + 1 >= end) {
             // ---- end of the item (or of this team's part)
             const int b = at.b, h = at.h;
             const bool whole = done && first == 0;
@@ -769,21 +791,13 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             }
             fence_proxy_async_smem();                // what was written into the stage comes before the next copies
         }
-        if (mask || !full) fence_proxy_async_smem();
+        if (mask) fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.bar_empty[s]);
-        ++at.t;
-        if (done && i + 1 < n_mine) {
-            at.t = first = 0;
+        more = paged_step(p, at, sp, kTile, end);
+        if (done && more) {
+            first = 0;
             part_i = i + 1;
-            if (++at.rb == p.RB) {
-                at.rb = 0;
-                if (++at.h == p.Hkv) {
-                    at.h = 0;
-                    do sp = paged_seq_span(p, ++at.b, kTile);
-                    while (sp.n_tiles == 0);
-                }
-            }
             if (!set_up()) return;
         }
     }
@@ -791,8 +805,9 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 
 // Joins the parts of the items that more than one block worked on, in the order of the list, and
 // writes the rows of sequences that have no tiles.  One warp to a row, a lane to four columns (and,
-// with D = 64, the halves of the warp to every other part).  Launched so that its blocks may start
-// while the decode kernel's last ones run; they wait for its end first.
+// with D = 64, the halves of the warp to every other part).  Its blocks may start while the decode
+// kernel's last ones run (8.9 against 10.9 us a call of one sequence); the same for the kernels before
+// and after gained nothing.
 constexpr int kCombineWarps = 4;
 
 template <int D, int MT>
@@ -800,7 +815,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps)
 paged_combine_kernel(const __grid_constant__ PagedParams p) {
     constexpr int kRows = 16 * MT;
     constexpr int kPerRow = D / 4, kGroups = 32 / kPerRow;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_prerequisites();
     const int x = blockIdx.x % (p.Hkv * p.RB), b = blockIdx.x / (p.Hkv * p.RB);
     const int h = x / p.RB, rb = x - h * p.RB;
     const int lane = threadIdx.x & 31;
@@ -809,11 +824,11 @@ paged_combine_kernel(const __grid_constant__ PagedParams p) {
     if (rb * 64 + r >= p.R) return;
     const int chunk = p.prefix[p.B + 1], in_b = p.prefix[b];
     const int n_tiles = paged_seq_span(p, b, PagedCfg<D>::kTile).n_tiles;
-    const int first = in_b + x * n_tiles;
+    const int first = in_b + x * paged_item(n_tiles);          // the item's place in the list
     float M = -INFINITY, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     if (n_tiles > 0) {
-        const int from = first / chunk, to = (first + n_tiles - 1) / chunk;
+        const int from = (first + kPagedItemCost) / chunk, to = (first + paged_item(n_tiles) - 1) / chunk;
         if (from == to) return;                        // one block had the whole item
         auto row_of = [&](int s) { return (2 * (size_t)s + (first > s * chunk)) * kRows + r; };
         for (int s = from + lane; s <= to; s += 32) M = fmaxf(M, p.part_ml[row_of(s) * 2]);

@@ -15,6 +15,7 @@
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
+#include "attn_fwd.cuh"
 #include "paging.h"
 
 namespace gpt_attn {
