@@ -19,6 +19,7 @@
 #include "attn_fwd.cuh"
 #include "gpt_attn.h"
 #include "paged_decode.cuh"
+#include "paged_decode_tc.cuh"
 #include "pages.cuh"
 #include "qk_prologue.cuh"
 #include "tmap_cache.h"
@@ -557,15 +558,16 @@ int check_cache(PagedPools* c, const gpt_attn_paged_cache* a) {
 
 bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
 
-// Row blocks of an item and 16-row tiles of a block of the paged decode kernel.
+// How an item's rows are cut: up to 32 go through the kernel on warp-level products, more through the one on
+// tcgen05 tiles of 128 rows (at %RULE).
 struct PagedShape {
-    int R, RB, MT;
+    int R, block, RB;             // rows of an item, of a row block, row blocks
 };
 PagedShape paged_shape(int H, int Hkv, int N) {
     PagedShape s;
     s.R = H / Hkv * N;
-    s.RB = (s.R + 63) / 64;
-    s.MT = s.R <= 16 ? 1 : (s.R <= 32 ? 2 : 4);
+    s.block = s.R <= 16 ? 16 : (s.R <= 32 ? 32 : kPagedTcRows);
+    s.RB = (s.R + s.block - 1) / s.block;
     return s;
 }
 
@@ -581,26 +583,30 @@ int check_paged_shape(int B, int H, int Hkv, int N, int D) {
 // workspace is sized by them.
 constexpr int kPagedBlocks = 148, kPagedAllTeams = kPagedTeams * kPagedBlocks;
 
-template <int D, int MT>
-int launch_paged(const PagedParams& p, int grid, cudaStream_t st) {
-    const size_t smem = sizeof(PagedSmem<D>) + 1024;
+template <int D, int kTile, int kRows, typename Kern>
+int launch_paged_kernels(Kern kernel, unsigned threads, size_t smem, const PagedParams& p, int grid, cudaStream_t st) {
     CUtensorMap mk, mv;
     const int rows = p.n_pages * p.Hkv * p.page.d, box = 1 << p.box_log2;
-    if (!make_tmap_rows(&mk, p.k, rows, D, box) || !make_tmap_rows(&mv, p.v, rows, D, box) ||
-        !set_smem(paged_decode_kernel<D, MT>, smem))
+    if (!make_tmap_rows(&mk, p.k, rows, D, box) || !make_tmap_rows(&mv, p.v, rows, D, box) || !set_smem(kernel, smem))
         return GPT_ATTN_ERR_CUDA;
-    paged_decode_kernel<D, MT><<<grid, kPagedThreads, smem, st>>>(mk, mv, p);
+    kernel<<<grid, threads, smem, st>>>(mk, mv, p);
     if (cudaGetLastError() != cudaSuccess) return GPT_ATTN_ERR_CUDA;
-    const int item_rows = p.R < 16 * MT ? p.R : 16 * MT;
+    const int item_rows = p.R < kRows ? p.R : kRows;
     const dim3 cgrid((unsigned)(p.B * p.Hkv * p.RB), (unsigned)((item_rows + kCombineWarps - 1) / kCombineWarps));
-    return launch_dependent(paged_combine_kernel<D, MT>, cgrid, 32 * kCombineWarps, 0, st, p) ? GPT_ATTN_OK
-                                                                                              : GPT_ATTN_ERR_CUDA;
+    return launch_dependent(paged_combine_kernel<D, kTile, kRows>, cgrid, 32 * kCombineWarps, 0, st, p) ? GPT_ATTN_OK
+                                                                                                        : GPT_ATTN_ERR_CUDA;
 }
 
 template <int D>
-int launch_paged_d(const PagedParams& p, int MT, int grid, cudaStream_t st) {
-    return MT == 1 ? launch_paged<D, 1>(p, grid, st) : MT == 2 ? launch_paged<D, 2>(p, grid, st)
-                                                               : launch_paged<D, 4>(p, grid, st);
+int launch_paged(const PagedParams& p, int block, int grid, cudaStream_t st) {
+    if (block == kPagedTcRows)
+        return launch_paged_kernels<D, kPagedTcTile, kPagedTcRows>(paged_decode_tc_kernel<D>, kPagedTcThreads,
+                                                                   sizeof(PagedTcSmem<D>) + 1024, p, grid, st);
+    constexpr int kTile = PagedCfg<D>::kTile;
+    const size_t smem = sizeof(PagedSmem<D>) + 1024;
+    if (block == 16)
+        return launch_paged_kernels<D, kTile, 16>(paged_decode_kernel<D, 1>, kPagedThreads, smem, p, grid, st);
+    return launch_paged_kernels<D, kTile, 32>(paged_decode_kernel<D, 2>, kPagedThreads, smem, p, grid, st);
 }
 
 // Strides of n [b, h, n, d] tensors from the C ABI (nullptr: contiguous); as for layouts.
@@ -822,7 +828,7 @@ int gpt_attn_decode(const void* q, const void* k_cache, const void* v_cache, con
 
 size_t gpt_attn_paged_decode_workspace_bytes(int B, int H, int Hkv, int N, int D) {
     if (check_paged_shape(B, H, Hkv, N, D) != GPT_ATTN_OK) return 0;
-    const size_t rows = (size_t)16 * paged_shape(H, Hkv, N).MT;
+    const size_t rows = paged_shape(H, Hkv, N).block;
     return 2 * (size_t)kPagedAllTeams * rows * (D + 2) * sizeof(float) + ((size_t)B + 2) * sizeof(int);
 }
 
@@ -857,8 +863,8 @@ int gpt_attn_paged_decode(const void* q, const gpt_attn_paged_cache* cache, cons
     p.q_str = st[0];
     p.o_str = st[1];
     p.part_o = static_cast<float*>(workspace);
-    p.part_ml = p.part_o + 2 * (size_t)kPagedAllTeams * 16 * s.MT * D;
-    p.prefix = reinterpret_cast<int*>(p.part_ml + 2 * (size_t)kPagedAllTeams * 16 * s.MT * 2);
+    p.part_ml = p.part_o + 2 * (size_t)kPagedAllTeams * s.block * D;
+    p.prefix = reinterpret_cast<int*>(p.part_ml + 2 * (size_t)kPagedAllTeams * s.block * 2);
     p.B = B;
     p.H = H;
     p.Hkv = c.Hkv;
@@ -880,13 +886,13 @@ int gpt_attn_paged_decode(const void* q, const gpt_attn_paged_cache* cache, cons
     p.q_flip = scale < 0.f ? 0x80008000u : 0u;
     p.timeout_ns = wait_timeout_ns();
     // No more blocks than the tables can name tiles; places in the list of them have to fit an int.
-    const int tile = D == 64 ? PagedCfg<64>::kTile : PagedCfg<128>::kTile;
+    const int tile = s.block == kPagedTcRows || D == 128 ? kPagedTcTile : PagedCfg<64>::kTile;
     const long long items = (long long)B * c.Hkv * s.RB, tiles = (c.cap + tile - 1) / tile + kPagedItemCost;
     if (items > 0x7fffffffLL / tiles) return GPT_ATTN_ERR_SHAPE;
     const long long most = items * tiles;
     const int grid = (int)(most < kPagedBlocks ? most : kPagedBlocks);
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    return D == 64 ? launch_paged_d<64>(p, s.MT, grid, cs) : launch_paged_d<128>(p, s.MT, grid, cs);
+    return D == 64 ? launch_paged<64>(p, s.block, grid, cs) : launch_paged<128>(p, s.block, grid, cs);
 }
 
 int gpt_attn_paged_append(const gpt_attn_paged_cache* cache, const void* k_new, const void* v_new, int N,

@@ -106,16 +106,15 @@ __device__ __forceinline__ uint32_t finite_bf16x2(uint32_t w) {
 template <int D>
 struct PagedCfg {
     static constexpr int kTile = D == 64 ? 128 : 64;              // keys of a tile
-    static constexpr int kWords = kTile / 32;
     static constexpr int kTileBytes = kTile * D * 2;              // of its keys: 16 KB
     static constexpr int kStages = 3;
 };
 
 // Byte offset of 16-byte chunk c of row r in a tile as TMA's 128-byte swizzle lays it out: 64 columns
 // of all rows after one another.
-template <int D>
+template <int kTile>
 __device__ __forceinline__ uint32_t paged_at(int r, int c) {
-    return (c >> 3) * (PagedCfg<D>::kTile * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+    return (c >> 3) * (kTile * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
 // A place in the list: tile t of item (sequence b, key head h, row block rb), number `pos` of the list.
@@ -178,17 +177,119 @@ struct PagedSmem {
     int abort;
 };
 
-// One of the two producer warps of a team, for its keys (which = 0) or values (1): walks the team's
-// piece of the list, up to place `end`, one tile a step.  Such a warp issues nearly alone, at 6 to 8 cycles an
-// instruction and some 80 a load, so instructions count here: one warp for both, with integer
-// divisions and the table's entries awaited where they were looked up, bounded the kernel.
-template <int D>
-__device__ __forceinline__ void paged_produce(const PagedParams& p, const CUtensorMap* tm, PagedTeam<D>& sm, int which,
-                                              int end, const AbortCtl& ac) {
-    using C = PagedCfg<D>;
-    constexpr int kTile = C::kTile, kWords = C::kWords, kStages = C::kStages;
+// One warp works out the tree of sequence b: each node takes over the ancestors of the node it points at
+// and points where that one does, so 6 rounds reach 64 nodes up.
+__device__ __forceinline__ void paged_tree(const PagedParams& p, int b, unsigned long long* anc, int* depth) {
     const int lane = threadIdx.x & 31;
-    PagedAt at = sm.start;
+    unsigned long long a[2];
+    int up[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int n = lane + 32 * e, to = n < p.N ? __ldg(p.parents + (size_t)b * p.N + n) : -1;
+        a[e] = 1ull << n;
+        up[e] = to < n ? to : -1;
+    }
+#pragma unroll 1
+    for (int step = 1; step < p.N; step *= 2) {
+        unsigned long long more[2];
+        int next[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int from = max(up[e], 0);
+            const unsigned long long a0 = __shfl_sync(0xffffffffu, a[0], from & 31), a1 = __shfl_sync(0xffffffffu, a[1], from & 31);
+            const int u0 = __shfl_sync(0xffffffffu, up[0], from & 31), u1 = __shfl_sync(0xffffffffu, up[1], from & 31);
+            more[e] = up[e] < 0 ? 0 : (from < 32 ? a0 : a1);
+            next[e] = up[e] < 0 ? -1 : (from < 32 ? u0 : u1);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            a[e] |= more[e];
+            up[e] = next[e];
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        anc[lane + 32 * e] = a[e];
+        depth[lane + 32 * e] = __popcll(a[e]) - 1;
+    }
+}
+
+// Cuts the list into the teams' pieces.  Team g of block x is number g * blocks + x, so that short lists
+// take an SM a piece.  Every thread of the block takes part; the teams' places to start at are written
+// where there are any, and read after the call.
+struct PagedPiece {
+    int chunk, all;               // length of a piece, and of the list
+};
+
+template <int kTile, int kThreads>
+__device__ __forceinline__ PagedPiece paged_cut(const PagedParams& p, int* scan, PagedAt* start0, PagedAt* start1) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int total = 0, mine = 0, upto = 0;               // lengths of all sequences; of sequence b, and up to its end
+    auto count = [&](int base) {
+        const int b = base + threadIdx.x;
+        const int n_tiles = b < p.B ? paged_seq_span(p, b, kTile).n_tiles : 0;
+        mine = upto = n_tiles > 0 ? paged_item(n_tiles) * p.Hkv * p.RB : 0;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, upto, off);
+            if (lane >= off) upto += y;
+        }
+        __syncthreads();
+        if (lane == 31) scan[warp] = upto;
+        __syncthreads();
+        upto += total;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+            const int x = scan[w];
+            if (w < warp) upto += x;
+            total += x;
+        }
+    };
+    for (int base = 0; base < p.B; base += kThreads) count(base);
+    const int chunk = paged_chunk(total, kPagedTeams * gridDim.x, 1), all = total;
+    auto find = [&](int base) {
+        const int b = base + threadIdx.x;
+        if (b >= p.B) return;
+        for (int g = 0; g < kPagedTeams; ++g) {
+            const long long begin = (long long)chunk * (g * gridDim.x + blockIdx.x);
+            if (begin >= upto - mine && begin < upto) {
+                const int len = paged_item(paged_seq_span(p, b, kTile).n_tiles), in_b = (int)begin - (upto - mine);
+                const int x = in_b / len, in_x = in_b - x * len;              // the item, and the place in it
+                (g ? *start1 : *start0) = PagedAt{b, x / p.RB, x % p.RB, max(in_x - kPagedItemCost, 0),
+                                              (int)begin + max(kPagedItemCost - in_x, 0)};
+            }
+        }
+        if (blockIdx.x == 0) p.prefix[b] = upto - mine;
+    };
+    if (p.B <= kThreads) {
+        find(0);
+    } else {
+        total = 0;
+        for (int base = 0; base < p.B; base += kThreads) {
+            count(base);
+            find(base);
+        }
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        p.prefix[p.B] = all;
+        p.prefix[p.B + 1] = chunk;
+    }
+    __syncthreads();
+    return PagedPiece{chunk, all};
+}
+
+// One of the two producer warps of a team, for its keys (which = 0) or values (1): walks the team's
+// piece of the list from `at` up to place `end`, one tile a step, through kStages slots at `slots`,
+// `stride` bytes apart.  The keys' producer also describes each tile in the ring `tiles` of kRing (and
+// arrives on its `tile_full`, if the ring has barriers of its own).  Such a warp issues nearly alone, at 6
+// to 8 cycles an instruction and some 80 a load, so instructions count here: one warp for both, with
+// integer divisions and the table's entries awaited where they were looked up, bounded the kernel.
+template <int D, int kTile, int kStages, int kRing>
+__device__ __forceinline__ void paged_produce(const PagedParams& p, const CUtensorMap* tm, int which, PagedAt at, int end,
+                                              uint8_t* slots, int stride, uint64_t* bar_full, uint64_t* bar_empty,
+                                              PagedTile* tiles, uint64_t* tile_full, const AbortCtl& ac) {
+    constexpr int kWords = kTile / 32, kTileBytes = kTile * D * 2;
+    const int lane = threadIdx.x & 31;
     PagedSpan sp = paged_seq_span(p, at.b, kTile);
     const int box = 1 << p.box_log2, boxes = kTile >> p.box_log2, past = p.n_pages * p.Hkv * p.page.d;
     const int* table = p.table + (size_t)at.b * p.max_pages;
@@ -260,25 +361,28 @@ __device__ __forceinline__ void paged_produce(const PagedParams& p, const CUtens
             for (int w = 0; w < kWords; ++w)
                 if (w * 32 < boxes) look_up(w);
         }
-        if (i >= kStages && !warp_wait(&sm.bar_empty[s], lap ^ 1, ac)) break;
+        if (i >= kStages && !warp_wait(&bar_empty[s], lap ^ 1, ac)) break;
         if (lane == 0) {
-            if (which == 0) sm.tile[s] = d;
-            mbar_arrive_expect_tx(&sm.bar_full[s], C::kTileBytes);
+            if (which == 0) {
+                tiles[i % kRing] = d;
+                if (tile_full) mbar_arrive(&tile_full[i % kRing]);
+            }
+            mbar_arrive_expect_tx(&bar_full[s], kTileBytes);
         }
         __syncwarp();
-        uint8_t* dst = sm.kv[s] + which * C::kTileBytes;
+        uint8_t* dst = slots + s * stride;
 #pragma unroll
         for (int w = 0; w < kWords; ++w) {
             const int j = lane + w * 32;
             if (w * 32 >= boxes || j >= boxes) continue;
 #pragma unroll
             for (int c = 0; c < D / 64; ++c)
-                tma_load_2d(dst + c * kTile * 128 + (j << p.box_log2) * 128, tm, &sm.bar_full[s], c * 64,
+                tma_load_2d(dst + c * kTile * 128 + (j << p.box_log2) * 128, tm, &bar_full[s], c * 64,
                             row[w] < 0 ? past : row[w]);
         }
     }
     // the copies in flight land before the block's shared memory is given up
-    for (int j = max(0, i - kStages); j < i; ++j) mbar_wait_drain(&sm.bar_full[j % kStages], (j / kStages) & 1, p.timeout_ns);
+    for (int j = max(0, i - kStages); j < i; ++j) mbar_wait_drain(&bar_full[j % kStages], (j / kStages) & 1, p.timeout_ns);
 }
 
 template <int D, int MT>
@@ -292,7 +396,6 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     constexpr int NT = kKeys / 8;
     constexpr int kChunks = D / 8;                   // 16-byte chunks of a row
     constexpr int kRows = 16 * MT;
-    constexpr int kWarps = kPagedThreads / 32;
     extern __shared__ uint8_t smem_raw[];
     PagedSmem<D>& block = *reinterpret_cast<PagedSmem<D>*>(smem_align1024(smem_raw));
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -319,71 +422,24 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         }
     }
 
-    // ---- the teams' pieces of the list.  Team g of block x is number g * blocks + x, so that short
-    // lists take an SM a piece.
-    int total = 0, mine = 0, upto = 0;               // lengths of all sequences; of sequence b, and up to its end
-    auto count = [&](int base) {
-        const int b = base + threadIdx.x;
-        const int n_tiles = b < p.B ? paged_seq_span(p, b, kTile).n_tiles : 0;
-        mine = upto = n_tiles > 0 ? paged_item(n_tiles) * p.Hkv * p.RB : 0;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, upto, off);
-            if (lane >= off) upto += y;
-        }
-        __syncthreads();
-        if (lane == 31) block.scan[warp] = upto;
-        __syncthreads();
-        upto += total;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const int x = block.scan[w];
-            if (w < warp) upto += x;
-            total += x;
-        }
-    };
-    for (int base = 0; base < p.B; base += kPagedThreads) count(base);
-    const int chunk = paged_chunk(total, kPagedTeams * gridDim.x, 1), all = total;
-    auto find = [&](int base) {
-        const int b = base + threadIdx.x;
-        if (b >= p.B) return;
-        for (int g = 0; g < kPagedTeams; ++g) {
-            const long long begin = (long long)chunk * (g * gridDim.x + blockIdx.x);
-            if (begin >= upto - mine && begin < upto) {
-                const int len = paged_item(paged_seq_span(p, b, kTile).n_tiles), in_b = (int)begin - (upto - mine);
-                const int x = in_b / len, in_x = in_b - x * len;              // the item, and the place in it
-                block.team[g].start = PagedAt{b, x / p.RB, x % p.RB, max(in_x - kPagedItemCost, 0),
-                                              (int)begin + max(kPagedItemCost - in_x, 0)};
-            }
-        }
-        if (blockIdx.x == 0) p.prefix[b] = upto - mine;
-    };
-    if (p.B <= kPagedThreads) {
-        find(0);
-    } else {
-        total = 0;
-        for (int base = 0; base < p.B; base += kPagedThreads) {
-            count(base);
-            find(base);
-        }
-    }
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
-        p.prefix[p.B] = all;
-        p.prefix[p.B + 1] = chunk;
-    }
-    __syncthreads();
+    const PagedPiece piece = paged_cut<kTile, kPagedThreads>(p, block.scan, &block.team[0].start, &block.team[1].start);
 
     // warps of team 0, of team 1, then keys' and values' producers of team 0, of team 1
     static_assert(kPagedTeams == 2, "two producers to a team make a warpgroup");
     const int extra = warp - kPagedTeams * kPagedTeamWarps;
     const int g = extra < 0 ? warp / kPagedTeamWarps : extra / 2;
     const int team_no = g * gridDim.x + blockIdx.x;
-    const int end = (int)min((long long)all, (long long)chunk * (team_no + 1));
-    const bool none = (long long)chunk * team_no >= all || block.team[g].start.pos >= end;
+    const int end = (int)min((long long)piece.all, (long long)piece.chunk * (team_no + 1));
+    const bool none = (long long)piece.chunk * team_no >= piece.all || block.team[g].start.pos >= end;
     const AbortCtl ac{&block.abort, p.timeout_ns};
     if (extra >= 0) {
         regs_dec<kPagedProducerRegs>();
-        if (!none) paged_produce<D>(p, extra & 1 ? &tm_v : &tm_k, block.team[g], extra & 1, end, ac);
+        if (!none) {
+            PagedTeam<D>& t = block.team[g];
+            paged_produce<D, kTile, kStages, kStages>(p, extra & 1 ? &tm_v : &tm_k, extra & 1, t.start, end,
+                                                      t.kv[0] + (extra & 1) * C::kTileBytes, 2 * C::kTileBytes, t.bar_full,
+                                                      t.bar_empty, t.tile, nullptr, ac);
+        }
         return;
     }
     regs_inc<kPagedTeamRegs>();
@@ -428,45 +484,11 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 raw[c][j] = live ? __ldg(reinterpret_cast<const uint4*>(src + c * 64)) : make_uint4(0u, 0u, 0u, 0u);
         }
         if (p.parents && at.b != cur_b) {
-            // The tree of this sequence, by the first warp: each node takes over the ancestors of the node
-            // it points at and points where that one does, so 6 rounds reach 64 nodes up.  The other
-            // buffer may still be read; the one before it is not, since all have passed that tree's join.
+            // The tree of this sequence, by the first warp.  The other buffer may still be read; the one
+            // before it is not, since all have passed that tree's join.
             tree ^= cur_b >= 0;
             cur_b = at.b;
-            if (w4 == 0) {
-                unsigned long long a[2];
-                int up[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int n = lane + 32 * e, to = n < p.N ? __ldg(p.parents + (size_t)at.b * p.N + n) : -1;
-                    a[e] = 1ull << n;
-                    up[e] = to < n ? to : -1;
-                }
-#pragma unroll 1
-                for (int step = 1; step < p.N; step *= 2) {
-                    unsigned long long more[2];
-                    int next[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int from = max(up[e], 0);
-                        const unsigned long long a0 = __shfl_sync(0xffffffffu, a[0], from & 31),
-                                                 a1 = __shfl_sync(0xffffffffu, a[1], from & 31);
-                        const int u0 = __shfl_sync(0xffffffffu, up[0], from & 31), u1 = __shfl_sync(0xffffffffu, up[1], from & 31);
-                        more[e] = up[e] < 0 ? 0 : (from < 32 ? a0 : a1);
-                        next[e] = up[e] < 0 ? -1 : (from < 32 ? u0 : u1);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        a[e] |= more[e];
-                        up[e] = next[e];
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    sm.anc[tree][lane + 32 * e] = a[e];
-                    sm.depth[tree][lane + 32 * e] = __popcll(a[e]) - 1;
-                }
-            }
+            if (w4 == 0) paged_tree(p, at.b, sm.anc[tree], sm.depth[tree]);
             if (!join()) return false;
         }
         if (at.rb != cur_rb) {
@@ -531,7 +553,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             const int key = kb + (lane & 7) + ((lane >> 4) << 3);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t at = k_addr + paged_at<D>(key, kk * 2 + ((lane >> 3) & 1));
+                const uint32_t at = k_addr + paged_at<kTile>(key, kk * 2 + ((lane >> 3) & 1));
 #pragma unroll
                 for (int n = 0; n < NT; n += 2) {
                     uint32_t b4[4];
@@ -614,7 +636,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             for (int c = partial ? lane : kKeys * kChunks; c < kKeys * kChunks; c += 32) {
                 const int key = kb + c / kChunks;
                 if (!((t.seen[key >> 5] >> (key & 31)) & 1))
-                    *reinterpret_cast<uint4*>(vt + paged_at<D>(key, c % kChunks)) = make_uint4(0u, 0u, 0u, 0u);
+                    *reinterpret_cast<uint4*>(vt + paged_at<kTile>(key, c % kChunks)) = make_uint4(0u, 0u, 0u, 0u);
             }
             __syncwarp();
         } else if (mask) {
@@ -649,7 +671,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 for (int n = 0; n < D / 8; ++n)
 #pragma unroll 1
                     for (int kk = 0; kk < kKeys; ++kk) {
-                        const uint32_t w = *reinterpret_cast<const uint32_t*>(vt + paged_at<D>(kb + kk, n) + (lane & 3) * 4);
+                        const uint32_t w = *reinterpret_cast<const uint32_t*>(vt + paged_at<kTile>(kb + kk, n) + (lane & 3) * 4);
                         if (!not_finite(w)) continue;
                         const float x0 = __uint_as_float(w << 16), x1 = __uint_as_float(w & 0xffff0000u);
 #pragma unroll
@@ -679,7 +701,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 #pragma unroll
                 for (int n = 0; n < D / 16; ++n) {
                     uint32_t b4[4];
-                    ldmatrix4_trans(b4, v_addr + paged_at<D>(key, n * 2 + (lane >> 4)) + kk * 16 * 128);
+                    ldmatrix4_trans(b4, v_addr + paged_at<kTile>(key, n * 2 + (lane >> 4)) + kk * 16 * 128);
                     mma_16816(oacc[2 * n], pf[kk], b4[0], b4[1]);
                     mma_16816(oacc[2 * n + 1], pf[kk], b4[2], b4[3]);
                 }
@@ -810,10 +832,9 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 // and after gained nothing.
 constexpr int kCombineWarps = 4;
 
-template <int D, int MT>
+template <int D, int kTile, int kRows>
 __global__ void __launch_bounds__(32 * kCombineWarps)
 paged_combine_kernel(const __grid_constant__ PagedParams p) {
-    constexpr int kRows = 16 * MT;
     constexpr int kPerRow = D / 4, kGroups = 32 / kPerRow;
     wait_prerequisites();
     const int x = blockIdx.x % (p.Hkv * p.RB), b = blockIdx.x / (p.Hkv * p.RB);
@@ -821,9 +842,9 @@ paged_combine_kernel(const __grid_constant__ PagedParams p) {
     const int lane = threadIdx.x & 31;
     const int r = blockIdx.y * kCombineWarps + (threadIdx.x >> 5);
     const int c = lane % kPerRow, g = lane / kPerRow;
-    if (rb * 64 + r >= p.R) return;
+    if (r >= kRows || rb * kRows + r >= p.R) return;
     const int chunk = p.prefix[p.B + 1], in_b = p.prefix[b];
-    const int n_tiles = paged_seq_span(p, b, PagedCfg<D>::kTile).n_tiles;
+    const int n_tiles = paged_seq_span(p, b, kTile).n_tiles;
     const int first = in_b + x * paged_item(n_tiles);          // the item's place in the list
     float M = -INFINITY, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -866,7 +887,7 @@ paged_combine_kernel(const __grid_constant__ PagedParams p) {
         }
     }
     if (g > 0) return;
-    const int row = rb * 64 + r, head = h * p.G + row / p.N, node = row % p.N;
+    const int row = rb * kRows + r, head = h * p.G + row / p.N, node = row % p.N;
     const bool any = l != 0.f;
     const float inv = any ? 1.f / l : 0.f;
     __nv_bfloat16* dst = p.o + b * p.o_str.b + (long long)head * p.o_str.h + node * p.o_str.t + c * 4;
