@@ -42,7 +42,8 @@ struct PagedTcTeam {
     PagedTile tile[kRing];
     uint64_t tile_full[kRing];
     uint64_t k_full[kSlots], k_empty[kSlots], v_full[kSlots], v_empty[kSlots];
-    uint64_t q_full, q_empty;     // the item's rows are in; all its S are done
+    uint64_t q_first;             // the first item's rows are in
+    uint64_t q_full, q_empty;     // the next item's rows are in; all S of an item are done
     uint64_t s_full[2], p_full[2], o_done[2];                     // of tiles in either S buffer
     uint64_t o_free;              // the item's O has been read
     uint64_t bar_join, bar_drain;
@@ -68,50 +69,74 @@ __device__ __forceinline__ bool paged_next_item(const PagedParams& p, PagedAt& a
     return paged_step(p, at, sp, tile, end);
 }
 
-// Row warp: each item's rows into the Q tile, K-major with the 128-byte swizzle; row r of the block at
-// tile row (r + first) % 128.
+// A team's pass over the values of a tile some rows of which are not to be used: unseen rows are cleared
+// and, if `check`, infinities and NaN of the others looked for.  Two threads to a row;
+// not unrolled, since it runs a few times a call and its instructions are waited for (61 against 59 us).
+template <int D, int kTile>
+__device__ __forceinline__ bool paged_clean(uint8_t* v, const PagedTile& t, int tid, bool check) {
+    constexpr int kPerRow = kPagedTeam / kTile, kMine = D / 8 / kPerRow;      // threads to a row, 16-byte chunks of each
+    const int key = tid / kPerRow, c0 = tid % kPerRow * kMine;
+    bool odd = false;
+    if (!((t.seen[key >> 5] >> (key & 31)) & 1)) {
+#pragma unroll 1
+        for (int c = 0; c < kMine; ++c) *reinterpret_cast<uint4*>(v + paged_at<kTile>(key, c0 + c)) = make_uint4(0u, 0u, 0u, 0u);
+    } else if (check) {
+#pragma unroll 1
+        for (int c = 0; c < kMine; ++c) {
+            const uint4 x = *reinterpret_cast<const uint4*>(v + paged_at<kTile>(key, c0 + c));
+            odd = odd || not_finite(x.x) || not_finite(x.y) || not_finite(x.z) || not_finite(x.w);
+        }
+    }
+    return odd;
+}
+
+// The rows of item `at` into the Q tile, K-major with the 128-byte swizzle; row r of the block at tile row
+// (r + first) % 128.  Warp `part` of `parts` takes every parts-th group of 16 rows.
 template <int D>
-__device__ __forceinline__ void paged_tc_rows(const PagedParams& p, PagedTcTeam<D>& sm, int first, int end,
-                                              const AbortCtl& ac) {
+__device__ __forceinline__ void paged_tc_rows(const PagedParams& p, uint8_t* q, const PagedAt& at, const PagedSpan& sp,
+                                              int first, int part, int parts) {
     const int lane = threadIdx.x & 31;
-    PagedAt at = sm.start;
-    PagedSpan sp = paged_seq_span(p, at.b, kPagedTcTile);
-    bool more = true;
-    for (int item = 0; more; ++item) {
-        if (item > 0 && !warp_wait(&sm.q_empty, (item - 1) & 1, ac)) return;
-        const int r0 = at.rb * kPagedTcRows, n = min(p.R - r0, kPagedTcRows);
-        // a row's 64 columns to 8 lanes
-        for (int base = 0; base < n; base += 16) {
-            uint4 raw[D / 64][4];
+    const int r0 = at.rb * kPagedTcRows, n = min(p.R - r0, kPagedTcRows);
+    for (int base = part * 16; base < n; base += parts * 16) {
+        uint4 raw[D / 64][4];                        // a row's 64 columns to 8 lanes
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int r = base + j * 4 + (lane >> 3), hd = p.by_n.div(r0 + r), nd = r0 + r - hd * p.N;
-                const bool live = r < n && nd < sp.n;
-                const __nv_bfloat16* src = p.q + at.b * p.q_str.b + (long long)(at.h * p.G + hd) * p.q_str.h +
-                                           nd * p.q_str.t + (lane & 7) * 8;
+        for (int j = 0; j < 4; ++j) {
+            const int r = base + j * 4 + (lane >> 3), hd = p.by_n.div(r0 + r), nd = r0 + r - hd * p.N;
+            const bool live = r < n && nd < sp.n;
+            const __nv_bfloat16* src = p.q + at.b * p.q_str.b + (long long)(at.h * p.G + hd) * p.q_str.h + nd * p.q_str.t +
+                                       (lane & 7) * 8;
 #pragma unroll
-                for (int c = 0; c < D / 64; ++c)
-                    raw[c][j] = live ? __ldg(reinterpret_cast<const uint4*>(src + c * 64)) : make_uint4(0u, 0u, 0u, 0u);
-            }
+            for (int c = 0; c < D / 64; ++c)
+                raw[c][j] = live ? __ldg(reinterpret_cast<const uint4*>(src + c * 64)) : make_uint4(0u, 0u, 0u, 0u);
+        }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int r = base + j * 4 + (lane >> 3), row = (r + first) % kPagedTcRows;
-                if (r >= kPagedTcRows) continue;
+        for (int j = 0; j < 4; ++j) {
+            const int r = base + j * 4 + (lane >> 3), row = (r + first) % kPagedTcRows;
 #pragma unroll
-                for (int c = 0; c < D / 64; ++c) {
-                    uint4 x = raw[c][j];
-                    x.x = x.x & p.q_keep ^ p.q_flip;
-                    x.y = x.y & p.q_keep ^ p.q_flip;
-                    x.z = x.z & p.q_keep ^ p.q_flip;
-                    x.w = x.w & p.q_keep ^ p.q_flip;
-                    *reinterpret_cast<uint4*>(sm.q + c * kPagedTcRows * 128 + row * 128 + (((lane & 7) ^ (row & 7)) << 4)) = x;
-                }
+            for (int c = 0; c < D / 64; ++c) {
+                uint4 x = raw[c][j];
+                x.x = x.x & p.q_keep ^ p.q_flip;
+                x.y = x.y & p.q_keep ^ p.q_flip;
+                x.z = x.z & p.q_keep ^ p.q_flip;
+                x.w = x.w & p.q_keep ^ p.q_flip;
+                *reinterpret_cast<uint4*>(q + c * kPagedTcRows * 128 + row * 128 + (((lane & 7) ^ (row & 7)) << 4)) = x;
             }
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.q_full);
-        more = paged_next_item(p, at, sp, kPagedTcTile, end);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+}
+
+// Row warp: brings in the rows of each item after the first once S of the last one is done.
+template <int D>
+__device__ __forceinline__ void paged_tc_next_rows(const PagedParams& p, PagedTcTeam<D>& sm, int first, int end,
+                                                   const AbortCtl& ac) {
+    PagedAt at = sm.start;
+    PagedSpan sp = paged_seq_span(p, at.b, kPagedTcTile);
+    for (int item = 0; paged_next_item(p, at, sp, kPagedTcTile, end); ++item) {
+        if (!warp_wait(&sm.q_empty, item & 1, ac)) return;
+        paged_tc_rows<D>(p, sm.q, at, sp, first, 0, 1);
+        if ((threadIdx.x & 31) == 0) mbar_arrive(&sm.q_full);
     }
 }
 
@@ -128,7 +153,7 @@ __device__ __forceinline__ void paged_tc_mma(const PagedParams& p, PagedTcTeam<D
     PagedSpan sp = paged_seq_span(p, at.b, kPagedTcTile);
     int s_item = 0;                                  // items S has begun
     auto issue_s = [&](int u, bool first, bool last) -> bool {
-        if (first && !mbar_wait(&sm.q_full, s_item++ & 1, ac)) return false;
+        if (first && !(s_item++ == 0 ? mbar_wait(&sm.q_first, 0, ac) : mbar_wait(&sm.q_full, s_item & 1, ac))) return false;
         const int s = u % kSlots;
         if (!mbar_wait(&sm.k_full[s], (u / kSlots) & 1, ac)) return false;
         if (u >= 2 && !mbar_wait(&sm.o_done[u & 1], ((u >> 1) - 1) & 1, ac)) return false;  // P of tile u - 2 was here
@@ -182,7 +207,6 @@ template <int D>
 __device__ __forceinline__ void paged_tc_softmax(const PagedParams& p, PagedTcTeam<D>& sm, uint32_t tmem, int g, int team_no,
                                                  int end, const AbortCtl& ac) {
     constexpr int kSlots = PagedTcTeam<D>::kSlots, kRing = PagedTcTeam<D>::kRing, kTile = kPagedTcTile;
-    constexpr int kChunks = D / 8;
     const int tid = threadIdx.x - g * kPagedTeam, lane = tid & 31, w4 = tid >> 5;
     const int r_loc = (tid + 64 * g) % kPagedTcRows;
     const uint32_t t_lane = tmem + ((uint32_t)(w4 * 32) << 16), t_s = t_lane + 128;
@@ -222,6 +246,9 @@ __device__ __forceinline__ void paged_tc_softmax(const PagedParams& p, PagedTcTe
         for (int w = 0; w < D / 32; ++w) up[w] = down[w] = 0;
         return true;
     };
+    // the first item's rows: the row warp alone would take them 16 at a time
+    paged_tc_rows<D>(p, sm.q, at, sp, 64 * g, w4, kPagedTeamWarps);
+    if (lane == 0) mbar_arrive(&sm.q_first);
     if (!set_up()) return;
     bool more = true, begin = true;                  // begin: the item's first tile here
     for (int u = 0; more; ++u) {
@@ -297,19 +324,9 @@ __device__ __forceinline__ void paged_tc_softmax(const PagedParams& p, PagedTcTe
         if (mask) {
             const int slot = u % kSlots;
             if (!warp_wait(&sm.v_full[slot], (u / kSlots) & 1, ac)) return;
-            uint4* rows = reinterpret_cast<uint4*>(sm.v[slot]);
-            bool odd = false;
-#pragma unroll 2
-            for (int c = tid; c < kTile * kChunks; c += kPagedTeam) {
-                const int key = (c >> 3) & (kTile - 1);
-                if (!((t.seen[key >> 5] >> (key & 31)) & 1)) {
-                    rows[c] = make_uint4(0u, 0u, 0u, 0u);
-                } else if (p.N > 1) {
-                    const uint4 x = rows[c];
-                    odd = odd || not_finite(x.x) || not_finite(x.y) || not_finite(x.z) || not_finite(x.w);
-                }
-            }
-            if (p.N > 1) {
+            const bool check = sp.differs(t.key0, kTile, p.window);
+            bool odd = paged_clean<D, kTile>(sm.v[slot], t, tid, check);
+            if (check) {
                 odd = __any_sync(0xffffffffu, odd);
                 int(&any)[kPagedTeamWarps] = sm.odd[joins & 1];   // a warp may be a join ahead of the readers
                 if (lane == 0) any[w4] = odd;
@@ -447,6 +464,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
                 mbar_init(&t.v_empty[s], 1);
             }
             for (int s = 0; s < Team::kRing; ++s) mbar_init(&t.tile_full[s], 1);
+            mbar_init(&t.q_first, kPagedTeamWarps);
             mbar_init(&t.q_full, 1);
             mbar_init(&t.q_empty, 1);
             for (int b = 0; b < 2; ++b) {
@@ -497,7 +515,7 @@ paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_co
         } else if (warp < 14) {
             if (lane == 0) paged_tc_mma<D>(p, t, tmem + g * 256, end, ac);
         } else {
-            paged_tc_rows<D>(p, t, 64 * g, end, ac);
+            paged_tc_next_rows<D>(p, t, 64 * g, end, ac);
         }
     } else {
         regs_inc<kPagedTcSoftmaxRegs>();

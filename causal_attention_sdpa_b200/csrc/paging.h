@@ -45,6 +45,11 @@ struct PagedSpan {
     GPT_ATTN_HD bool needs_any(int key, int n, int sinks) const {
         return key < end && (key + n > w_lo || key < sinks);
     }
+    // Whether some node sees one of `n_keys` keys from `key` on that another does not: a new token, or one at
+    // the window's lower edge.
+    GPT_ATTN_HD bool differs(int key, int n_keys, int window) const {
+        return n > 1 && (key + n_keys > L || (window > 0 && key + n_keys > w_lo && key <= L + n - 1 - window));
+    }
 };
 
 GPT_ATTN_HD PagedSpan paged_span(int len, int n_new, int cap, int window, int sinks, int tile) {

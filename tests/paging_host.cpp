@@ -35,5 +35,8 @@ int pg_box(int page) { return paged_box(page); }
 int pg_needs_any(int len, int n, int page, int max_pages, int window, int sinks, int key, int box) {
     return paged_span(len, n, page * max_pages, window, sinks, 64).needs_any(key, box, sinks);
 }
+int pg_differs(int len, int n, int page, int max_pages, int window, int sinks, int key, int n_keys) {
+    return paged_span(len, n, page * max_pages, window, sinks, 64).differs(key, n_keys, window);
+}
 int pg_chunk(int total, int blocks, int least) { return paged_chunk(total, blocks, least); }
 }
