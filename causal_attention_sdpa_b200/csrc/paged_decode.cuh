@@ -3,27 +3,31 @@
 // groups of query heads, and optionally a window with sinks.
 //
 // The rows of one item are the N new tokens of the G query heads that share a key head: R = G * N
-// rows against the same keys, in blocks of up to 64.  A key and a value of D elements (4 D bytes)
-// serve 4 D R flops, R flops a byte, so up to some hundred rows HBM bounds the call, and the kernel
-// is built to keep loads in flight:
+// rows against the same keys.  A key and a value of D elements (4 D bytes) serve 4 D R flops, R flops a
+// byte, so up to some hundred rows HBM bounds the call, and the kernel is built to keep loads in
+// flight.  This file has what both kernels share and the one for up to 32 rows; paged_decode_tc.cuh
+// has the one for more.
 //   - Keys and values come in tiles of 32 KB (128 keys of 64 elements, 64 of 128) through a ring of
-//     shared-memory stages.  A producer warp brings them with TMA, in boxes of as many rows as a page
+//     shared-memory stages.  Producer warps bring them with TMA, in boxes of as many rows as a page
 //     lets them be (the largest power of two that divides it, so a tile takes 8 boxes from pages of 16
 //     tokens, 128 from odd pages), one lane to a box.  Boxes that nobody sees and missing pages are
 //     not read but zero-filled.  A tile's pages are looked up while the tile before it is issued.
 //   - All (sequence, key head, row block) items form one list, each as long as its tiles and what it
 //     costs besides, cut into equal pieces, one to a team of warps (two teams to an SM): ragged batches
-//     and single long sequences fill the GPU alike.  The ring runs on across items.  A piece that holds a whole item writes O and lse;
-//     the others leave fp32 partial results, joined by paged_combine_kernel.
+//     and single long sequences fill the GPU alike.  The ring runs on across items.  A piece that holds
+//     a whole item writes O and lse; the others leave fp32 partial results, joined by
+//     paged_combine_kernel.
 //   - Four warps of a team compute: scores and P V on warp-level matrix instructions (16 rows x 16 keys
-//     a step; a tcgen05 tile has 128 rows, of which a call has 1 to 64), the softmax in registers
-//     between them.  With up to 16 rows each warp takes a quarter of a tile's keys, with a softmax
-//     state of its own, joined at the end of the item; with up to 32, each pair of warps 16 rows; with
-//     up to 64, each warp 16 rows and all keys.
+//     a step; a tcgen05 tile has 128 rows, of which these calls have 1 to 32), the softmax in registers
+//     between them.  With up to 16 rows each warp takes a quarter of a tile's keys, else each pair of
+//     warps 16 rows and each of them half of the keys; every warp has a softmax state of its own, joined
+//     at the end of the item.
 // A warp's steps on a tile depend on one another, so their latency counts, not their number: two teams
-// share one block because its warps can then have 208 registers each (two blocks with a producer each
-// put five warps on an SM sub-partition's registers and spilled: 90 us against 65 us at 16 streams of
-// 13 drafts, 24 query heads of 128 on 6 key heads, window 4096).
+// share one block because its warps can then have 208 registers each (blocks of one team put five warps
+// on an SM sub-partition's registers and spilled).
+// Measured on one B200: one token of 16 sequences of 16384 (6 heads of 128) 134 us, 6.0 TB/s; of 64
+// sequences of 4096 (12 heads of 64, pages of 16) 136 us, 5.9 TB/s; of 64 up to 1024 32 us, 3.9 TB/s; of
+// one of 777 9 us.  Some 11 us of a call are launches, the first loads and the join.
 // Statistics and accumulators are fp32; P is rounded to bf16 for the second product, as in the
 // forward kernel, while its sum is taken before the rounding.
 #pragma once
@@ -37,9 +41,12 @@ constexpr int kPagedTeams = 2;                                // of a block
 constexpr int kPagedTeamWarps = 4;
 constexpr int kPagedTeam = 32 * kPagedTeamWarps;
 constexpr int kPagedThreads = kPagedTeams * kPagedTeam + 128; // and a warpgroup with a producer warp for each team
-// What an item costs besides its tiles (its rows in, its states joined, its output), in tiles.  Pieces
-// are cut by tiles and items together: cut by tiles alone, those with an item's end in them ran on, %COST.
-constexpr int kPagedItemCost = 1;
+// What an item costs besides its tiles (its rows in, its states joined, its output), in tiles; pieces are
+// cut by tiles and items together, since those with an item's end in them ran on.  It grows with the
+// rows: 8 tiles with more than 16 of them (13 drafts over 16 streams, window 4096: 52.9 us, at 1 56.5, at 3
+// 54.1; 32 drafts over 8 contexts up to 8192: 43.3, 46.4, 45.1), else 1 (one token of 64 sequences up to
+// 1024: 32.2 us, at 3 32.0, at 8 33.4; of one sequence: 8.8, 9.3, 9.3).
+constexpr int paged_item_cost(int rows) { return rows > 16 ? 8 : 1; }
 // Registers of a thread: 168 at the launch, given up by the producers' warpgroup and taken by the teams.
 constexpr int kPagedProducerRegs = 88, kPagedTeamRegs = 208;
 
@@ -60,6 +67,7 @@ struct PagedParams {
     int B, H, Hkv, G, N;
     FastDiv by_n;                 // N
     int R, RB;                    // rows of an item, row blocks
+    int item_cost;
     FastDiv page;
     int box_log2;                 // log2 of the rows that one load brings
     int max_pages, n_pages, cap;
@@ -123,13 +131,13 @@ struct PagedAt {
 };
 
 // Length of an item of the list.
-__device__ __forceinline__ int paged_item(int n_tiles) { return n_tiles + kPagedItemCost; }
+__device__ __forceinline__ int paged_item(const PagedParams& p, int n_tiles) { return n_tiles + p.item_cost; }
 
 // On to the next tile; false (and nowhere) at the end of the piece.
 __device__ __forceinline__ bool paged_step(const PagedParams& p, PagedAt& at, PagedSpan& sp, int tile, int end) {
     ++at.pos;
     if (at.t + 1 == sp.n_tiles) {
-        at.pos += kPagedItemCost;
+        at.pos += p.item_cost;
         if (at.pos >= end) return false;
         at.t = 0;
         if (++at.rb == p.RB) {
@@ -176,6 +184,28 @@ struct PagedSmem {
     int scan[kPagedThreads / 32];
     int abort;
 };
+
+// A team's pass over the values of a tile some rows of which are not to be used: unseen rows are cleared
+// and, if `check`, infinities and NaN of the others looked for.  The pass
+// runs a few times a call, so that its instructions are waited for: not unrolled, the tcgen05 kernel
+// gains 2 us of 61; the other gains more from the schedule of its other loops beside the unrolled one.
+template <int D, int kTile, int kUnroll>
+__device__ __forceinline__ bool paged_clean(uint8_t* v, const PagedTile& t, int tid, bool check) {
+    constexpr int kPerRow = kPagedTeam / kTile, kMine = D / 8 / kPerRow;      // threads to a row, 16-byte chunks of each
+    const int key = tid / kPerRow, c0 = tid % kPerRow * kMine;
+    bool odd = false;
+    if (!((t.seen[key >> 5] >> (key & 31)) & 1)) {
+#pragma unroll kUnroll
+        for (int c = 0; c < kMine; ++c) *reinterpret_cast<uint4*>(v + paged_at<kTile>(key, c0 + c)) = make_uint4(0u, 0u, 0u, 0u);
+    } else if (check) {
+#pragma unroll kUnroll
+        for (int c = 0; c < kMine; ++c) {
+            const uint4 x = *reinterpret_cast<const uint4*>(v + paged_at<kTile>(key, c0 + c));
+            odd = odd || not_finite(x.x) || not_finite(x.y) || not_finite(x.z) || not_finite(x.w);
+        }
+    }
+    return odd;
+}
 
 // One warp works out the tree of sequence b: each node takes over the ancestors of the node it points at
 // and points where that one does, so 6 rounds reach 64 nodes up.
@@ -228,7 +258,7 @@ __device__ __forceinline__ PagedPiece paged_cut(const PagedParams& p, int* scan,
     auto count = [&](int base) {
         const int b = base + threadIdx.x;
         const int n_tiles = b < p.B ? paged_seq_span(p, b, kTile).n_tiles : 0;
-        mine = upto = n_tiles > 0 ? paged_item(n_tiles) * p.Hkv * p.RB : 0;
+        mine = upto = n_tiles > 0 ? paged_item(p, n_tiles) * p.Hkv * p.RB : 0;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, upto, off);
@@ -253,10 +283,10 @@ __device__ __forceinline__ PagedPiece paged_cut(const PagedParams& p, int* scan,
         for (int g = 0; g < kPagedTeams; ++g) {
             const long long begin = (long long)chunk * (g * gridDim.x + blockIdx.x);
             if (begin >= upto - mine && begin < upto) {
-                const int len = paged_item(paged_seq_span(p, b, kTile).n_tiles), in_b = (int)begin - (upto - mine);
+                const int len = paged_item(p, paged_seq_span(p, b, kTile).n_tiles), in_b = (int)begin - (upto - mine);
                 const int x = in_b / len, in_x = in_b - x * len;              // the item, and the place in it
-                (g ? *start1 : *start0) = PagedAt{b, x / p.RB, x % p.RB, max(in_x - kPagedItemCost, 0),
-                                              (int)begin + max(kPagedItemCost - in_x, 0)};
+                (g ? *start1 : *start0) = PagedAt{b, x / p.RB, x % p.RB, max(in_x - p.item_cost, 0),
+                                              (int)begin + max(p.item_cost - in_x, 0)};
             }
         }
         if (blockIdx.x == 0) p.prefix[b] = upto - mine;
@@ -411,7 +441,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         block.abort = 0;
         fence_barrier_init();
     }
-    if (MT < 4 && threadIdx.x < kRows) {
+    if (threadIdx.x < kRows) {
         block.row_head[threadIdx.x] = p.by_n.div(threadIdx.x);
         block.row_node[threadIdx.x] = threadIdx.x - p.by_n.div(threadIdx.x) * p.N;
     }
@@ -456,8 +486,14 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     float m[2], l[2];
     int lower[2];
     unsigned long long vis[2];                       // 0: no such row, or no such node
-    int node[2] = {0, 0}, head[2] = {0, 0};          // node, and head within the group, of the two rows; -1: no row
-    int cur_b = -1, cur_rb = -1, item = 0, tree = 0;
+    int node[2], head[2];                            // node, and head within the group, of the two rows; -1: no row
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int r = r_lo + 8 * e, hd = p.by_n.div(r);
+        head[e] = r < p.R ? hd : -1;
+        node[e] = r - hd * p.N;
+    }
+    int cur_b = -1, item = 0, tree = 0;
     uint32_t joins = 0, lap = 1;
     int s = -1;
     // a barrier of the team
@@ -475,7 +511,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         uint4 raw[D / 64][4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int r = at.rb * 64 + mt * 16 + j * 4 + (lane >> 3), hd = p.by_n.div(r), nd = r - hd * p.N;
+            const int r = mt * 16 + j * 4 + (lane >> 3), hd = p.by_n.div(r), nd = r - hd * p.N;
             const bool live = r < p.R && nd < sp.n;
             const __nv_bfloat16* src = p.q + at.b * p.q_str.b + (long long)(at.h * p.G + hd) * p.q_str.h + nd * p.q_str.t +
                                        (lane & 7) * 8;
@@ -490,15 +526,6 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             cur_b = at.b;
             if (w4 == 0) paged_tree(p, at.b, sm.anc[tree], sm.depth[tree]);
             if (!join()) return false;
-        }
-        if (at.rb != cur_rb) {
-            cur_rb = at.rb;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int r = at.rb * 64 + r_lo + 8 * e, hd = p.by_n.div(r);
-                head[e] = r < p.R ? hd : -1;
-                node[e] = r - hd * p.N;
-            }
         }
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
@@ -642,14 +669,20 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         } else if (mask) {
             uint4* rows = reinterpret_cast<uint4*>(vt);
             bool odd = false;
+            if constexpr (MT == 2) {
+                odd = paged_clean<D, kTile, D / 8>(vt, t, tid, sp.differs(t.key0, kTile, p.window));
+            } else {
+                // chunk by chunk: 134 against 155 us with the pass above for one token of 16 sequences of 16384
+                // (6 heads of 128), which does not even come here, by how the rest is scheduled beside it
 #pragma unroll 2
-            for (int c = tid; c < kTile * kChunks; c += kPagedTeam) {
-                const int key = (c >> 3) & (kTile - 1);
-                if (!((t.seen[key >> 5] >> (key & 31)) & 1)) {
-                    rows[c] = make_uint4(0u, 0u, 0u, 0u);
-                } else if (p.N > 1) {
-                    const uint4 x = rows[c];
-                    odd = odd || not_finite(x.x) || not_finite(x.y) || not_finite(x.z) || not_finite(x.w);
+                for (int c = tid; c < kTile * kChunks; c += kPagedTeam) {
+                    const int key = (c >> 3) & (kTile - 1);
+                    if (!((t.seen[key >> 5] >> (key & 31)) & 1)) {
+                        rows[c] = make_uint4(0u, 0u, 0u, 0u);
+                    } else if (p.N > 1) {
+                        const uint4 x = rows[c];
+                        odd = odd || not_finite(x.x) || not_finite(x.y) || not_finite(x.z) || not_finite(x.w);
+                    }
                 }
             }
             odd = __any_sync(0xffffffffu, odd);
@@ -724,93 +757,66 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             }
             // a piece has at most two partial items: the one it starts in and the one it ends in
             const size_t part = (2 * (size_t)team_no + (part_i > 0)) * kRows;
-            if constexpr (KS > 1) {
-                // The warps that share rows join their states through the stage itself, which they
-                // have all read by then.  (The statistics alternate between two buffers: a warp may
-                // be an item ahead of those that still read the last one's.)
-                const int par = item++ & 1;
-                if ((lane & 3) == 0) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        sm.m[par][w4][(lane >> 2) + 8 * e] = m[e];
-                        sm.l[par][w4][(lane >> 2) + 8 * e] = l[e];
-                    }
-                }
-                if (!join()) return;
-                float2* state = reinterpret_cast<float2*>(sm.kv[s]);
+            // The warps that share rows join their states through the stage itself, which they
+            // have all read by then.  (The statistics alternate between two buffers: a warp may
+            // be an item ahead of those that still read the last one's.)
+            const int par = item++ & 1;
+            if ((lane & 3) == 0) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int r = (lane >> 2) + 8 * e;
-                    if (vis[e] == 0) continue;
-#pragma unroll
-                    for (int n = 0; n < D / 8; ++n)
-                        state[(w4 * 16 + r) * (D / 2) + ((n * 4 + (lane & 3)) ^ ((r & 3) * 4))] =
-                            make_float2(oacc[n][2 * e], oacc[n][2 * e + 1]);
-                }
-                if (!join()) return;
-                for (int at = tid; at < p.R * (D / 4); at += kPagedTeam) {       // R <= kRows: one row block
-                    const int r = at / (D / 4), c = at % (D / 4);
-                    const int w0 = (r / 16) * KS, rr = r % 16;
-                    float M = -INFINITY, sum = 0.f;
-#pragma unroll
-                    for (int w = 0; w < KS; ++w) M = fmaxf(M, sm.m[par][w0 + w][rr]);
-                    const float mu = M == -INFINITY ? 0.f : M;
-                    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                    for (int w = 0; w < KS; ++w) {
-                        const float lw = sm.l[par][w0 + w][rr];
-                        if (lw == 0.f) continue;     // a warp whose keys the row does not see wrote nothing of use
-                        const float f = ex2_approx(sm.m[par][w0 + w][rr] - mu);
-                        sum += lw * f;
-                        const float4 y = *reinterpret_cast<const float4*>(state + ((w0 + w) * 16 + rr) * (D / 2) +
-                                                                          ((c * 2) ^ ((rr & 3) * 4)));
-                        a.x += f * y.x;
-                        a.y += f * y.y;
-                        a.z += f * y.z;
-                        a.w += f * y.w;
-                    }
-                    const bool any = sum != 0.f;
-                    if (whole) {
-                        const int hd = h * p.G + block.row_head[r], nd = block.row_node[r];
-                        __nv_bfloat16* dst = p.o + b * p.o_str.b + hd * p.o_str.h + nd * p.o_str.t + c * 4;
-                        const float inv = any ? 1.f / sum : 0.f;
-                        *reinterpret_cast<uint2*>(dst) =
-                            make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
-                        if (c == 0)
-                            p.lse[((size_t)b * p.H + hd) * p.N + nd] =
-                                any ? (M + log2f(sum)) * 0.69314718055994531f : -INFINITY;
-                    } else {
-                        *reinterpret_cast<float4*>(p.part_o + (part + r) * D + c * 4) = a;
-                        if (c == 0) *reinterpret_cast<float2*>(p.part_ml + (part + r) * 2) = make_float2(M, sum);
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int r = r_lo + 8 * e;
-                    if (head[e] < 0) continue;
-                    const bool any = l[e] != 0.f;
-                    if (whole) {
-                        const int hd = h * p.G + head[e];
-                        __nv_bfloat16* dst = p.o + b * p.o_str.b + hd * p.o_str.h + node[e] * p.o_str.t + (lane & 3) * 2;
-                        const float inv = any ? 1.f / l[e] : 0.f;
-#pragma unroll
-                        for (int n = 0; n < D / 8; ++n)
-                            *reinterpret_cast<uint32_t*>(dst + n * 8) =
-                                any ? pack_bf16x2(oacc[n][2 * e] * inv, oacc[n][2 * e + 1] * inv) : 0u;
-                        if ((lane & 3) == 0)
-                            p.lse[((size_t)b * p.H + hd) * p.N + node[e]] =
-                                any ? (m[e] + log2f(l[e])) * 0.69314718055994531f : -INFINITY;
-                    } else {
-                        float* dst = p.part_o + (part + r) * D + (lane & 3) * 2;
-#pragma unroll
-                        for (int n = 0; n < D / 8; ++n)
-                            *reinterpret_cast<float2*>(dst + n * 8) = make_float2(oacc[n][2 * e], oacc[n][2 * e + 1]);
-                        if ((lane & 3) == 0)
-                            *reinterpret_cast<float2*>(p.part_ml + (part + r) * 2) = make_float2(m[e], l[e]);
-                    }
+                    sm.m[par][w4][(lane >> 2) + 8 * e] = m[e];
+                    sm.l[par][w4][(lane >> 2) + 8 * e] = l[e];
                 }
             }
+            if (!join()) return;
+            float2* state = reinterpret_cast<float2*>(sm.kv[s]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = (lane >> 2) + 8 * e;
+                if (vis[e] == 0) continue;
+#pragma unroll
+                for (int n = 0; n < D / 8; ++n)
+                    state[(w4 * 16 + r) * (D / 2) + ((n * 4 + (lane & 3)) ^ ((r & 3) * 4))] =
+                        make_float2(oacc[n][2 * e], oacc[n][2 * e + 1]);
+            }
+            if (!join()) return;
+            for (int at = tid; at < p.R * (D / 4); at += kPagedTeam) {       // R <= kRows: one row block
+                const int r = at / (D / 4), c = at % (D / 4);
+                const int w0 = (r / 16) * KS, rr = r % 16;
+                float M = -INFINITY, sum = 0.f;
+#pragma unroll
+                for (int w = 0; w < KS; ++w) M = fmaxf(M, sm.m[par][w0 + w][rr]);
+                const float mu = M == -INFINITY ? 0.f : M;
+                float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < KS; ++w) {
+                    const float lw = sm.l[par][w0 + w][rr];
+                    if (lw == 0.f) continue;     // a warp whose keys the row does not see wrote nothing of use
+                    const float f = ex2_approx(sm.m[par][w0 + w][rr] - mu);
+                    sum += lw * f;
+                    const float4 y = *reinterpret_cast<const float4*>(state + ((w0 + w) * 16 + rr) * (D / 2) +
+                                                                      ((c * 2) ^ ((rr & 3) * 4)));
+                    a.x += f * y.x;
+                    a.y += f * y.y;
+                    a.z += f * y.z;
+                    a.w += f * y.w;
+                }
+                const bool any = sum != 0.f;
+                if (whole) {
+                    const int hd = h * p.G + block.row_head[r], nd = block.row_node[r];
+                    __nv_bfloat16* dst = p.o + b * p.o_str.b + hd * p.o_str.h + nd * p.o_str.t + c * 4;
+                    const float inv = any ? 1.f / sum : 0.f;
+                    *reinterpret_cast<uint2*>(dst) =
+                        make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+                    if (c == 0)
+                        p.lse[((size_t)b * p.H + hd) * p.N + nd] =
+                            any ? (M + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+                } else {
+                    *reinterpret_cast<float4*>(p.part_o + (part + r) * D + c * 4) = a;
+                    if (c == 0) *reinterpret_cast<float2*>(p.part_ml + (part + r) * 2) = make_float2(M, sum);
+                }
+            }
+
             fence_proxy_async_smem();                // what was written into the stage comes before the next copies
         }
         if (mask) fence_proxy_async_smem();
@@ -845,11 +851,11 @@ paged_combine_kernel(const __grid_constant__ PagedParams p) {
     if (r >= kRows || rb * kRows + r >= p.R) return;
     const int chunk = p.prefix[p.B + 1], in_b = p.prefix[b];
     const int n_tiles = paged_seq_span(p, b, kTile).n_tiles;
-    const int first = in_b + x * paged_item(n_tiles);          // the item's place in the list
+    const int first = in_b + x * paged_item(p, n_tiles);          // the item's place in the list
     float M = -INFINITY, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     if (n_tiles > 0) {
-        const int from = (first + kPagedItemCost) / chunk, to = (first + paged_item(n_tiles) - 1) / chunk;
+        const int from = (first + p.item_cost) / chunk, to = (first + paged_item(p, n_tiles) - 1) / chunk;
         if (from == to) return;                        // one block had the whole item
         auto row_of = [&](int s) { return (2 * (size_t)s + (first > s * chunk)) * kRows + r; };
         for (int s = from + lane; s <= to; s += 32) M = fmaxf(M, p.part_ml[row_of(s) * 2]);

@@ -8,11 +8,12 @@
 // done, the values' once O is.  Another warp brings the next item's rows in while the last tile of this
 // one is in the softmax.
 //
-// What bounds it: a tile's softmax takes a warp some 1200 cycles whatever its rows, so what counts is
-// that all rows of an item share one tile, and that the two teams of a block do not wait for one
+// What bounds it: HBM for long items, else what comes before and after the tiles (rows, masks, joining).  A
+// tile's softmax takes a warp some 1600 cycles whatever its rows, so what counts is that all rows of an item share one tile, and that the two teams of a block do not wait for one
 // another: with 64 rows or fewer only two warps of a team have rows, and the second team's rows are put
 // at the other end of its tile, where the other two sub-partitions of the SM read them.
-// %MEASURED
+// Measured on one B200: 13 drafts over 16 streams up to 32768 (24 query heads on 6 of 128, window 4096) 52 us,
+// 4.0 TB/s; the same without a window over 16 contexts of 16384 167 us, 4.8 TB/s.
 //
 // Masks are words of 32 keys, as in the other kernel.  Rows that came along in a box unseen are cleared,
 // and infinities and NaN of drafts, which other nodes must not see through 0 * NaN, are cleared too and
@@ -67,27 +68,6 @@ __device__ __forceinline__ bool paged_next_item(const PagedParams& p, PagedAt& a
     at.pos += sp.n_tiles - 1 - at.t;
     at.t = sp.n_tiles - 1;
     return paged_step(p, at, sp, tile, end);
-}
-
-// A team's pass over the values of a tile some rows of which are not to be used: unseen rows are cleared
-// and, if `check`, infinities and NaN of the others looked for.  Two threads to a row;
-// not unrolled, since it runs a few times a call and its instructions are waited for (61 against 59 us).
-template <int D, int kTile>
-__device__ __forceinline__ bool paged_clean(uint8_t* v, const PagedTile& t, int tid, bool check) {
-    constexpr int kPerRow = kPagedTeam / kTile, kMine = D / 8 / kPerRow;      // threads to a row, 16-byte chunks of each
-    const int key = tid / kPerRow, c0 = tid % kPerRow * kMine;
-    bool odd = false;
-    if (!((t.seen[key >> 5] >> (key & 31)) & 1)) {
-#pragma unroll 1
-        for (int c = 0; c < kMine; ++c) *reinterpret_cast<uint4*>(v + paged_at<kTile>(key, c0 + c)) = make_uint4(0u, 0u, 0u, 0u);
-    } else if (check) {
-#pragma unroll 1
-        for (int c = 0; c < kMine; ++c) {
-            const uint4 x = *reinterpret_cast<const uint4*>(v + paged_at<kTile>(key, c0 + c));
-            odd = odd || not_finite(x.x) || not_finite(x.y) || not_finite(x.z) || not_finite(x.w);
-        }
-    }
-    return odd;
 }
 
 // The rows of item `at` into the Q tile, K-major with the 128-byte swizzle; row r of the block at tile row
@@ -325,7 +305,7 @@ __device__ __forceinline__ void paged_tc_softmax(const PagedParams& p, PagedTcTe
             const int slot = u % kSlots;
             if (!warp_wait(&sm.v_full[slot], (u / kSlots) & 1, ac)) return;
             const bool check = sp.differs(t.key0, kTile, p.window);
-            bool odd = paged_clean<D, kTile>(sm.v[slot], t, tid, check);
+            bool odd = paged_clean<D, kTile, 1>(sm.v[slot], t, tid, check);
             if (check) {
                 odd = __any_sync(0xffffffffu, odd);
                 int(&any)[kPagedTeamWarps] = sm.odd[joins & 1];   // a warp may be a join ahead of the readers
