@@ -462,11 +462,12 @@ def gpt_attn_bwd_sinks(q, k, v, o, lse, dO, window=0, sinks=0, scale=None, head_
     torch = _t()
     B, H, T, D, shape, dev = _check_sinks_call(q, doc_start, head_windows, lse)
     _check_views(dev, shape, q=q, k=k, v=v, o=o, dO=dO)
-    dtype, device = q.dtype, q.device
-    dq = torch.empty(shape, dtype=dtype, device=device) if dq is None else dq
-    dk = torch.empty(shape, dtype=dtype, device=device) if dk is None else dk
-    dv = torch.empty(shape, dtype=dtype, device=device) if dv is None else dv
-    _check_views(dev, shape, dq=dq, dk=dk, dv=dv)
+    device = q.device
+    if dq is None and dk is None and dv is None:
+        dq, dk, dv = torch.empty((3, B, H, T, D), dtype=q.dtype, device=device).unbind(0)     # one allocation
+    else:
+        dq, dk, dv = (torch.empty(shape, dtype=q.dtype, device=device) if t is None else t for t in (dq, dk, dv))
+        _check_views(dev, shape, dq=dq, dk=dk, dv=dv)
     if workspace is None:
         top = max(head_windows) if head_windows is not None else window
         workspace = torch.empty(max(gpt_attn_bwd_sinks_workspace_bytes(B, H, T, D, top, sinks), 16),
@@ -726,9 +727,10 @@ def gpt_attn_pages_compact(table, refs, workspace=None, stream=None):
     """Packs the n pages in use into places 0 to n - 1.  Returns (new_table, new_refs, pairs int32
     [P // 2, 2], moves int32 [1]); gpt_attn_pages_copy(k, v, pairs, n_pairs=moves) moves the pages."""
     S, M, P, dev = _check_state(table, refs)
-    new_table, new_refs = _t().empty_like(table), _t().empty_like(refs)
-    pairs = _int32_out("pairs", None, (P // 2, 2), table)
-    moves = _int32_out("moves", None, (1,), table)
+    n = P // 2
+    results = _t().empty(2 * n + S * M + P + 1, dtype=_t().int32, device=table.device)        # one allocation
+    pairs, new_table, new_refs, moves = results.split((2 * n, S * M, P, 1))
+    pairs, new_table = pairs.view(n, 2), new_table.view(S, M)
     ws = _pages_workspace(workspace, S, M, P, table)
     _launch("gpt_attn_pages_compact", dev, stream, table.data_ptr(), refs.data_ptr(), S, M, P, new_table.data_ptr(),
             new_refs.data_ptr(), pairs.data_ptr(), moves.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
