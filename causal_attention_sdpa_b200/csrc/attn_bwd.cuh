@@ -61,7 +61,11 @@ struct BwdParams {
     float scale_log2;       // scale * log2(e)
     float scale;
     uint64_t timeout_ns;
-    int n_sink_tiles;       // with sinks and without documents: key tiles of a head that hold them
+    int units;              // work units in all
+    // With sinks and without documents, else n_s = 0: the cut of the key tiles that hold them, and where
+    // those of more than one piece leave their sums: [BH, n_s, most pieces, dV and dK, 128, D]
+    SinkCut cut;
+    float* part;
 };
 
 // Last query tile that sees key tile kt of head bh (window W).
@@ -72,11 +76,34 @@ __device__ __forceinline__ int bwd_last_tile(const BwdParams& p, const Mask& mas
     return bwd_last_query_tile(kt, p.n_tiles, W);
 }
 
-// Work unit u: head and key tile.  With sinks and without documents the tiles that hold sinks go first.
-template <typename Mask>
-__device__ __forceinline__ void bwd_list_item(const BwdParams& p, int u, int& bh, int& kt) {
-    if (Mask::kSinks && p.n_sink_tiles > 0) list_item_sinks(u, p.BH, p.n_tiles, p.n_sink_tiles, p.tail, bh, kt);
-    else list_item(u, p.BH, p.n_tiles, p.tail, bh, kt);
+// Work unit u: head, key tile and its query tiles [lo, lo + n); part: where its sums go, or nullptr for dK
+// and dV themselves.
+struct BwdUnit {
+    int bh, kt, lo, n, W;
+    float* part;
+};
+template <int D, typename Mask>
+__device__ __forceinline__ BwdUnit bwd_unit_of(const BwdParams& p, const Mask& mask, int u) {
+    BwdUnit w;
+    w.part = nullptr;
+    if constexpr (Mask::kCut) {
+        int piece;
+        list_item_sinks(u, p.BH, p.n_tiles, p.cut, p.tail, w.bh, w.kt, piece);
+        w.W = mask.head_window(w.bh);
+        w.lo = w.kt + piece * p.cut.len;
+        w.n = bwd_last_tile(p, mask, w.bh, w.kt, w.W) - w.lo + 1;
+        if (w.kt < p.cut.n_s && p.cut.pieces(w.kt, p.n_tiles) > 1) {
+            w.n = min(w.n, p.cut.len);
+            w.part = p.part + (((size_t)w.bh * p.cut.n_s + w.kt) * p.cut.most + piece) * (2 * kTile * D);
+        }
+        return w;
+    }
+    if (Mask::kSinks && p.cut.n_s > 0) list_item_sinks(u, p.BH, p.n_tiles, p.cut, p.tail, w.bh, w.kt, w.n);
+    else list_item(u, p.BH, p.n_tiles, p.tail, w.bh, w.kt);
+    w.W = mask.head_window(w.bh);
+    w.lo = w.kt;
+    w.n = bwd_last_tile(p, mask, w.bh, w.kt, w.W) - w.kt + 1;
+    return w;
 }
 
 // With sinks: whether key `key` of head bh is a sink, hence seen by every later query of its
@@ -201,6 +228,41 @@ attn_bwd_prep_kernel(const __nv_bfloat16* __restrict__ o, const __nv_bfloat16* _
     }
 }
 
+// dK and dV of the key tiles that were cut: the pieces' sums, added in order.  G = D / 8 threads to a row.
+template <int D>
+__global__ void __launch_bounds__(256)
+attn_sink_join_kernel(const float* __restrict__ part, __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv,
+                      const Strides dk_str, const Strides dv_str, const SinkCut cut, int n_tiles, int T, int H) {
+    constexpr int G = D / 8;
+    const int kt = blockIdx.y % cut.n_s, bh = blockIdx.y / cut.n_s, n = cut.pieces(kt, n_tiles);
+    const int x = blockIdx.x * (256 / G) + threadIdx.x / G, which = x / kTile, r = x % kTile, g = threadIdx.x % G;
+    const int key = kt * kTile + r;
+    if (n <= 1 || which > 1 || key >= T) return;
+    const size_t piece = 2 * kTile * D;
+    const float4* from = reinterpret_cast<const float4*>(part + ((size_t)bh * cut.n_s + kt) * cut.most * piece +
+                                                         (size_t)x * D + g * 8);
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+        const float4 y = from[i * (piece / 4)], z = from[i * (piece / 4) + 1];
+        a.x += y.x;
+        a.y += y.y;
+        a.z += y.z;
+        a.w += y.w;
+        b.x += z.x;
+        b.y += z.y;
+        b.z += z.z;
+        b.w += z.w;
+    }
+    uint4 o;
+    o.x = pack_bf16x2(a.x, a.y);
+    o.y = pack_bf16x2(a.z, a.w);
+    o.z = pack_bf16x2(b.x, b.y);
+    o.w = pack_bf16x2(b.z, b.w);
+    __nv_bfloat16* to = which == 0 ? dv + dv_str.row(bh, H, key) : dk + dk_str.row(bh, H, key);
+    *reinterpret_cast<uint4*>(to + g * 8) = o;
+}
+
 // dQ = bf16(scale * acc): G = D / 8 threads per row of the accumulator [BH, T, D], 8 elements
 // (two 16-byte loads, one 16-byte store) each, written to dQ's layout.  One division per thread
 // finds the row's head.
@@ -244,13 +306,12 @@ attn_bwd_serial_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
     const int lane = threadIdx.x & 31;
     // Blocks of one head are adjacent in launch order (its Q, dO and dQ rows stay in
     // L2 across its key tiles); key tile 0 sees the most query tiles and launches first.
-    int bh, kt;
-    bwd_list_item<Mask>(p, blockIdx.x, bh, kt);   // unit list order of schedule.h
+    const BwdUnit unit = bwd_unit_of<D>(p, mask, blockIdx.x);   // unit list order of schedule.h
+    const int bh = unit.bh, kt = unit.kt;
     const int k0 = kt * kTile;
-    const int qt_lo = kt;
-    const int W = mask.head_window(bh);
-    const int qt_hi = bwd_last_tile(p, mask, bh, kt, W);
-    const int n_q = qt_hi - qt_lo + 1;
+    const int qt_lo = unit.lo;
+    const int W = unit.W;
+    const int n_q = unit.n;
 
     if (threadIdx.x == 0) {
         mbar_init(&sm.bar_kv, 1);
@@ -527,6 +588,17 @@ attn_bwd_serial_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                     uint32_t rr[32];
                     tmem_ld32(t_lane + col0 + c * 32, rr);
                     tmem_wait_ld();
+                    if constexpr (Mask::kCut) {
+                        if (unit.part) {
+                            float* part = unit.part + (size_t)(which * kTile + r) * D + c * 32;
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4)
+                                *reinterpret_cast<float4*>(part + e) =
+                                    make_float4(__uint_as_float(rr[e]) * mul, __uint_as_float(rr[e + 1]) * mul,
+                                                __uint_as_float(rr[e + 2]) * mul, __uint_as_float(rr[e + 3]) * mul);
+                            continue;
+                        }
+                    }
                     uint32_t pk[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 2)

@@ -90,19 +90,14 @@ struct Bwd64Smem {
 
 struct Bwd64Unit {
     int bh, kt, k0, qt_lo, n_q, W;
+    float* part;
 };
 
-// Work unit u of the list (schedule.h): head bh, key tile kt, and the n_q query tiles
-// [kt, kt + n_q) that see it.
+// Work unit u of the list (schedule.h): head bh, key tile kt, and the n_q query tiles from qt_lo on.
 template <typename Mask>
 __device__ __forceinline__ Bwd64Unit bwd64_unit(int u, const BwdParams& p, const Mask& mask) {
-    Bwd64Unit w;
-    bwd_list_item<Mask>(p, u, w.bh, w.kt);
-    w.W = mask.head_window(w.bh);
-    w.n_q = bwd_last_tile(p, mask, w.bh, w.kt, w.W) - w.kt + 1;
-    w.k0 = w.kt * kTile;
-    w.qt_lo = w.kt;
-    return w;
+    const BwdUnit x = bwd_unit_of<64>(p, mask, u);
+    return Bwd64Unit{x.bh, x.kt, x.kt * kTile, x.lo, x.n, x.W, x.part};
 }
 
 template <typename Mask>
@@ -125,7 +120,7 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const int total_units = p.BH * p.n_tiles;
+    const int total_units = p.units;
 
     if (threadIdx.x == 0) {
         for (int b = 0; b < 2; ++b) {
@@ -471,6 +466,17 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                         uint32_t rr[32];
                         tmem_ld32(t_lane + col0 + c * 32, rr);
                         tmem_wait_ld();
+                        if constexpr (Mask::kCut) {
+                            if (w.part) {
+                                float* part = w.part + (size_t)(which * kTile + r) * 64 + c * 32;
+#pragma unroll
+                                for (int e = 0; e < 32; e += 4)
+                                    *reinterpret_cast<float4*>(part + e) =
+                                        make_float4(__uint_as_float(rr[e]) * mul, __uint_as_float(rr[e + 1]) * mul,
+                                                    __uint_as_float(rr[e + 2]) * mul, __uint_as_float(rr[e + 3]) * mul);
+                                continue;
+                            }
+                        }
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             uint32_t v4[4];
@@ -489,10 +495,12 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 mbar_arrive(&sm.bar_dkdv_staged);
                 if (warp == 12 && lane == 0) {
                     if (!mbar_wait(&sm.bar_dkdv_staged, n & 1, ac)) return false;
-                    tma_store_4d(&tm_dv, sm.v[kb], 0, w.k0, w.bh % p.H, w.bh / p.H);
-                    tma_store_4d(&tm_dk, sm.k[kb], 0, w.k0, w.bh % p.H, w.bh / p.H);
-                    bulk_commit_group();
-                    bulk_wait_group_read0();
+                    if (!Mask::kCut || !w.part) {
+                        tma_store_4d(&tm_dv, sm.v[kb], 0, w.k0, w.bh % p.H, w.bh / p.H);
+                        tma_store_4d(&tm_dk, sm.k[kb], 0, w.k0, w.bh % p.H, w.bh / p.H);
+                        bulk_commit_group();
+                        bulk_wait_group_read0();
+                    }
                     mbar_arrive(&sm.bar_kv_empty[kb]);
                 }
                 return true;

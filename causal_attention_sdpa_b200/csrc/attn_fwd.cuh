@@ -66,7 +66,7 @@ struct WindowMask {
     // Lower bound of the keys query i sees (schedule.h row_lower).
     __device__ __forceinline__ int row_lower_of(int, int, int W, int i) const { return row_lower(i, W, 0); }
     static constexpr bool kDoc = false;
-    static constexpr bool kSinks = false;
+    static constexpr bool kSinks = false, kCut = false;
 };
 
 constexpr int kMaxHeadWindows = 64;   // per-head windows travel in the kernel parameters
@@ -85,7 +85,7 @@ struct MaskParams {
         return row_lower(i, W, d);
     }
     static constexpr bool kDoc = true;
-    static constexpr bool kSinks = false;
+    static constexpr bool kSinks = false, kCut = false;
 };
 
 // MaskParams with sinks: the first `sinks` tokens of a query's document stay visible past the
@@ -96,7 +96,12 @@ struct SinkMask : MaskParams {
     __device__ __forceinline__ int doc_of(int bh, int T, int i) const {
         return doc_start ? row_doc(i, __ldg(doc_start + (size_t)(bh / H) * T + (i < T ? i : T - 1))) : 0;
     }
-    static constexpr bool kSinks = true;
+    static constexpr bool kSinks = true, kCut = false;
+};
+
+// The same in a backward pass whose sink tiles are cut into pieces (schedule.h).
+struct CutSinkMask : SinkMask {
+    static constexpr bool kCut = true;
 };
 
 __device__ __forceinline__ int mask_window(const MaskParams& m, int bh) { return m.head_window(bh); }

@@ -312,6 +312,33 @@ WsLayout ws_layout(void* ws, int BH, int T, int D) {
     return w;
 }
 
+// The cut of the sink tiles, by the largest of the call's windows (0, or past T: not cut, as the call's
+// other heads are as long) and a B200's 148 SMs, so that the workspace can be sized without a device.
+SinkCut call_cut(int BH, int T, int window, int sinks) {
+    const int n_tiles = (T + kTile - 1) / kTile;
+    if (sinks <= 0) return make_cut(0, 1, n_tiles);
+    const bool reaches = window <= 0 || window >= T;
+    const SinkCut c = sink_cut(BH, n_tiles, reaches ? 1 : window, sinks < T ? sinks : T, 148);
+    return reaches ? make_cut(c.n_s, n_tiles, n_tiles) : c;
+}
+SinkCut launch_cut(int BH, int T, const SinkMask& sinks, const MaskParams& mask) {
+    int window = mask.head_windows ? 0 : mask.window;
+    for (int h = 0; mask.head_windows && h < mask.H; ++h) window = std::max(window, mask.win[h]);
+    return call_cut(BH, T, window, sinks.sinks);
+}
+
+// The pieces' sums, behind the rest of the workspace.
+size_t sink_part_bytes_of(const SinkCut& c, int BH, int D) {
+    return c.most > 1 ? (size_t)BH * c.n_s * c.most * 2 * kTile * D * sizeof(float) : 0;
+}
+size_t sink_part_bytes(int BH, int T, int D, int window, int sinks) {
+    return sink_part_bytes_of(call_cut(BH, T, window, sinks), BH, D);
+}
+size_t sink_part_at(int BH, int T, int D) { return (gpt_attn_bwd_workspace_bytes(BH, 1, T, D) + 255) / 256 * 256; }
+float* sink_part(void* ws, int BH, int T, int D) {
+    return reinterpret_cast<float*>(static_cast<char*>(ws) + sink_part_at(BH, T, D));
+}
+
 // SM count of the current device, cached per device.  Host threads may call the library at the
 // same time: the cache entries are atomics (every thread would store the same value).
 int sm_count() {
@@ -372,15 +399,17 @@ int launch_bwd_grads(const void* q, const void* k, const void* v, const void* do
     p.T_pad = w.T_pad;
     p.BH = BH;
     p.n_tiles = w.n_tiles;
-    p.n_sink_tiles = 0;
-    if (sinks && !mask.doc_start) p.n_sink_tiles = (int)std::min<long long>(p.n_tiles, ((long long)sinks->sinks + kTile - 1) / kTile);
-    p.tail = tail_heads(BH, std::max(1, p.n_tiles - p.n_sink_tiles), sm_count());
+    p.cut = make_cut(0, 1, w.n_tiles);
+    if (sinks && !mask.doc_start) p.cut = launch_cut(BH, T, *sinks, mask);
+    p.part = sink_part(ws, BH, T, D);
+    p.units = BH * (p.cut.units + w.n_tiles - p.cut.n_s);
+    p.tail = tail_heads(BH, std::max(1, w.n_tiles - p.cut.n_s), sm_count());
     p.lower2 = mask.doc_start ? w.lower2 : nullptr;
     p.last_qt = mask.doc_start ? w.last_qt : nullptr;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.scale = scale;
     p.timeout_ns = wait_timeout_ns();
-    const long long units = (long long)w.n_tiles * BH;
+    const int units = p.units;
     const unsigned grid = (unsigned)units;
     if constexpr (D == 64) {
         CUtensorMap mdq, mdk, mdv;
@@ -390,7 +419,11 @@ int launch_bwd_grads(const void* q, const void* k, const void* v, const void* do
         const size_t smem = sizeof(Bwd64Smem) + 1024;
         // persistent: one CTA per SM, work units taken from the counter in the workspace
         const unsigned pgrid = (unsigned)(units < sm_count() ? units : sm_count());
-        if (sinks) {
+        if (sinks && p.cut.most > 1) {
+            if (!set_smem(attn_bwd_kernel<CutSinkMask>, smem)) return GPT_ATTN_ERR_CUDA;
+            attn_bwd_kernel<CutSinkMask><<<pgrid, kBwd64Threads, smem, st>>>(mq, mk, mv, mdo, mdq, mdk, mdv, p,
+                                                                           CutSinkMask{*sinks});
+        } else if (sinks) {
             if (!set_smem(attn_bwd_kernel<SinkMask>, smem)) return GPT_ATTN_ERR_CUDA;
             attn_bwd_kernel<SinkMask><<<pgrid, kBwd64Threads, smem, st>>>(mq, mk, mv, mdo, mdq, mdk, mdv, p, *sinks);
         } else if (plain_window(mask)) {
@@ -405,7 +438,11 @@ int launch_bwd_grads(const void* q, const void* k, const void* v, const void* do
         CUtensorMap mdq;
         if (!make_tmap_f32_acc(&mdq, w.dq_acc, BH, T, D)) return GPT_ATTN_ERR_CUDA;
         const size_t smem = sizeof(BwdSmem<D>) + 1024;
-        if (sinks) {
+        if (sinks && p.cut.most > 1) {
+            if (!set_smem(attn_bwd_serial_kernel<D, CutSinkMask>, smem)) return GPT_ATTN_ERR_CUDA;
+            attn_bwd_serial_kernel<D, CutSinkMask><<<grid, kBwdThreads, smem, st>>>(mq, mk, mv, mdo, mdq, p,
+                                                                                  CutSinkMask{*sinks});
+        } else if (sinks) {
             if (!set_smem(attn_bwd_serial_kernel<D, SinkMask>, smem)) return GPT_ATTN_ERR_CUDA;
             attn_bwd_serial_kernel<D, SinkMask><<<grid, kBwdThreads, smem, st>>>(mq, mk, mv, mdo, mdq, p, *sinks);
         } else if (plain_window(mask)) {
@@ -417,7 +454,13 @@ int launch_bwd_grads(const void* q, const void* k, const void* v, const void* do
             attn_bwd_serial_kernel<D, MaskParams><<<grid, kBwdThreads, smem, st>>>(mq, mk, mv, mdo, mdq, p, mask);
         }
     }
-    return cudaGetLastError() == cudaSuccess ? GPT_ATTN_OK : GPT_ATTN_ERR_CUDA;
+    if (cudaGetLastError() != cudaSuccess) return GPT_ATTN_ERR_CUDA;
+    if (p.cut.most > 1) {
+        const dim3 jgrid(2 * kTile * (D / 8) / 256, (unsigned)(BH * p.cut.n_s));
+        attn_sink_join_kernel<D><<<jgrid, 256, 0, st>>>(p.part, p.dk, p.dv, L.dk, L.dv, p.cut, w.n_tiles, T, H);
+        if (cudaGetLastError() != cudaSuccess) return GPT_ATTN_ERR_CUDA;
+    }
+    return GPT_ATTN_OK;
 }
 
 int launch_dq_convert(void* dq, int B, int H, int T, int D, float scale, void* ws, const Layout& L, cudaStream_t st) {
@@ -757,9 +800,9 @@ int gpt_attn_bwd_dq_convert(void* dq, int B, int H, int T, int D, float scale, v
 }
 
 size_t gpt_attn_bwd_sinks_workspace_bytes(int B, int H, int T, int D, int window, int sinks) {
-    (void)window;
-    (void)sinks;
-    return gpt_attn_bwd_workspace_bytes(B, H, T, D);
+    const size_t plain = gpt_attn_bwd_workspace_bytes(B, H, T, D);
+    const size_t part = plain ? sink_part_bytes(B * H, T, D, window, sinks) : 0;
+    return part ? sink_part_at(B * H, T, D) + part : plain;
 }
 
 int gpt_attn_bwd_sinks(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dO,
@@ -779,6 +822,11 @@ int gpt_attn_bwd_sinks(const void* q, const void* k, const void* v, const void* 
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     SinkMask sm;
     const SinkMask* sp = sink_mask(&sm, m, sinks, H, T) ? &sm : nullptr;
+    if (sp && !m.doc_start) {
+        const SinkCut cut = launch_cut(B * H, T, sm, m);
+        if (cut.most > 1 && workspace_bytes < sink_part_at(B * H, T, D) + sink_part_bytes_of(cut, B * H, D))
+            return GPT_ATTN_ERR_WORKSPACE;
+    }
     sc = sp ? launch_bwd_delta(o, lse, dO, B, H, T, D, workspace, *sp, L, st)
             : launch_bwd_delta(o, lse, dO, B, H, T, D, workspace, m, L, st);
     if (sc != GPT_ATTN_OK) return sc;

@@ -161,17 +161,52 @@ GPT_ATTN_HD void list_item(int i, int BH, int n_cls, int tail, int& bh, int& cls
     }
 }
 
-// Backward item u when n_s of the n_cls key tiles of a head hold sinks, hence are seen by all later
-// query tiles where the others are seen by a window's worth: those go first, class-major, then the
-// list of the others.  In the plain order the last heads' sink tiles started late and ran on alone:
-// 540 us against 442 us at B=4 H=6 T=8192 D=128, window 1024, 4 sinks.
-GPT_ATTN_HD void list_item_sinks(int u, int BH, int n_cls, int n_s, int tail, int& bh, int& cls) {
-    if (u < BH * n_s) {
+// Backward with sinks and without documents: n_s of a head's n_cls key tiles hold sinks, hence are seen
+// by all later query tiles where the others are seen by a window's worth.  Those are cut into pieces of
+// `len` query tiles (n_cls: not cut), each a unit of its own with partial sums of dK and dV that are
+// added up afterwards, and their units go first, then the list of the others.  In the plain order the
+// last heads' sink tiles started late and ran on alone: 540 against 428 us at B=4 H=6 T=8192 D=128, window
+// 1024, 4 sinks, where nothing is cut.
+struct SinkCut {
+    int n_s, len;
+    int most, units;              // most pieces of a tile (1: nothing is cut), and units of a head's sink tiles
+    // Pieces of key tile kt.
+    GPT_ATTN_HD int pieces(int kt, int n_cls) const { return (n_cls - kt + len - 1) / len; }
+};
+
+GPT_ATTN_HD SinkCut make_cut(int n_s, int len, int n_cls) {
+    SinkCut c{n_s, len, 1, 0};
+    if (n_s > 0) c.most = c.pieces(0, n_cls);
+    for (int kt = 0; kt < n_s; ++kt) c.units += c.pieces(kt, n_cls);
+    return c;
+}
+
+// The cut for a window and sinks (both at least 1): a piece is as long as an SM's share of all units,
+// so that a sink tile does not outlast the rest (B=1 H=6 T=8192 D=128, window 512, 4 sinks, both passes: 145 us,
+// not cut 300; B=1 H=2 D=64, window 128: 46 and 157),
+// and no shorter than the unit of another key tile.
+GPT_ATTN_HD SinkCut sink_cut(int BH, int n_cls, int window, int sinks, int sms) {
+    const long long holds = ((long long)sinks + kTile - 1) / kTile;
+    const int n_s = holds < n_cls ? (int)holds : n_cls;
+    const long long reach = ((long long)window + kTile - 2) / kTile + 1;     // query tiles that see a key tile
+    const long long all = BH * ((long long)n_s * n_cls + (n_cls - n_s) * (reach < n_cls ? reach : n_cls));
+    long long len = (all + sms - 1) / sms;
+    if (len < reach) len = reach;
+    return make_cut(n_s, len < n_cls ? (int)len : n_cls, n_cls);
+}
+
+// Unit u of that order: head, key tile and piece (0 of the tiles that are not cut).
+GPT_ATTN_HD void list_item_sinks(int u, int BH, int n_cls, const SinkCut& cut, int tail, int& bh, int& cls, int& piece) {
+    const int first = BH * cut.units;
+    piece = 0;
+    if (u < first) {
         cls = u / BH;
         bh = u % BH;
+        if (cut.most <= 1) return;                            // one piece a tile
+        for (piece = cls, cls = 0; piece >= cut.pieces(cls, n_cls); ++cls) piece -= cut.pieces(cls, n_cls);
     } else {
-        list_item(u - BH * n_s, BH, n_cls - n_s, tail, bh, cls);
-        cls += n_s;
+        list_item(u - first, BH, n_cls - cut.n_s, tail, bh, cls);
+        cls += cut.n_s;
     }
 }
 

@@ -43,7 +43,14 @@ int snk_bwd_last(const int* ds, int T, int W, int sinks, int kt) {
         kt, n_tiles, sinks, [&](int qt) { return lower_at(ds, T, W, qt * kTile); },
         [&](int qt) { return doc_at(ds, T, qt * kTile); });
 }
-void snk_list_item(int u, int BH, int n_cls, int n_s, int tail, int* bh, int* cls) {
-    list_item_sinks(u, BH, n_cls, n_s, tail, *bh, *cls);
+// The cut of the sink tiles: n_s and len; returns the units of a head's sink tiles.
+int snk_cut(int BH, int n_cls, int window, int sinks, int* n_s, int* len) {
+    const SinkCut c = sink_cut(BH, n_cls, window, sinks, 148);
+    *n_s = c.n_s;
+    *len = c.len;
+    return c.units;
+}
+void snk_list_item(int u, int BH, int n_cls, int n_s, int len, int tail, int* bh, int* cls, int* piece) {
+    list_item_sinks(u, BH, n_cls, make_cut(n_s, len, n_cls), tail, *bh, *cls, *piece);
 }
 }

@@ -124,16 +124,31 @@ def test_any_document_starts_keep_the_roles_in_step(S):
             assert kt <= last < -(-T // TILE)
 
 
-@pytest.mark.parametrize("BH,n,n_s", [(1, 1, 1), (24, 64, 1), (5, 7, 3), (3, 4, 4), (100, 9, 2), (2, 30, 0)])
-def test_backward_order_takes_each_unit_once_and_sink_tiles_first(S, BH, n, n_s):
+@pytest.mark.parametrize("BH,n,W,sinks", [(1, 1, 1, 1), (24, 64, 1024, 4), (5, 7, 130, 300), (3, 4, 5, 10 ** 9),
+                                          (6, 64, 512, 4), (1, 64, 128, 4), (2, 64, 4000, 500), (100, 9, 128, 200)])
+def test_backward_order_takes_each_query_tile_once_and_sink_tiles_first(S, BH, n, W, sinks):
+    n_s, length = ctypes.c_int(), ctypes.c_int()
+    units = S.snk_cut(BH, n, W, min(sinks, n * TILE), ctypes.byref(n_s), ctypes.byref(length))
+    n_s, length = n_s.value, length.value
+    assert n_s == min(n, -(-sinks // TILE)) and 1 <= length <= n
+    assert length == n or length >= (W + TILE - 2) // TILE + 1      # no shorter than the other tiles' units
+    # the longest unit is no longer than another tile's or than an SM's share
+    reach = min(n, (W + TILE - 2) // TILE + 1)
+    share = -(-BH * (n_s * n + (n - n_s) * reach) // 148)
+    assert min(length, n) <= max(reach, share)
+    total = BH * (units + n - n_s)
     for tail in {1, BH // 2 + 1, BH}:
         seen = []
-        for u in range(BH * n):
-            bh, cls = ctypes.c_int(), ctypes.c_int()
-            S.snk_list_item(u, BH, n, n_s, tail, ctypes.byref(bh), ctypes.byref(cls))
-            seen.append((bh.value, cls.value))
-        assert sorted(seen) == [(b, c) for b in range(BH) for c in range(n)]
-        assert all(c < n_s for _, c in seen[:BH * n_s])
+        for u in range(total):
+            bh, cls, piece = ctypes.c_int(), ctypes.c_int(), ctypes.c_int()
+            S.snk_list_item(u, BH, n, n_s, length, tail, ctypes.byref(bh), ctypes.byref(cls), ctypes.byref(piece))
+            lo = cls.value + piece.value * length
+            hi = min(lo + length, n) if cls.value < n_s else cls.value + 1
+            assert lo < hi
+            seen += [(bh.value, cls.value, q) for q in range(lo, hi)]
+            assert (cls.value < n_s) == (u < BH * units)
+        want = [(b, c, q) for b in range(BH) for c in range(n) for q in (range(c, n) if c < n_s else [c])]
+        assert sorted(seen) == want
 
 
 # ------------------------------------------------------------------------------ refusals
@@ -147,6 +162,14 @@ def test_refusals():
     need = ga.gpt_attn_bwd_sinks_workspace_bytes(1, 2, 300, 64, 100, 4)
     assert need > 0
     assert ga.gpt_attn_bwd_sinks_workspace_bytes(1, 2, 300, 32, 100, 4) == 0
+    plain = ga.gpt_attn_bwd_workspace_bytes(1, 2, 300, 64)
+    assert need > plain == ga.gpt_attn_bwd_sinks_workspace_bytes(1, 2, 300, 64, 100, 0)
+    for window in (0, -1, 300, 2 ** 31 - 1):                        # nothing out of reach: no sinks, nothing cut
+        assert ga.gpt_attn_bwd_sinks_workspace_bytes(1, 2, 300, 64, window, 4) == plain
+    for window in (1, 128, 1000, 4000):                             # the cut's sums stay small
+        for sinks in (1, 300, 2 ** 31 - 1):
+            assert ga.gpt_attn_bwd_sinks_workspace_bytes(1, 2, 8192, 128, window, sinks) - \
+                ga.gpt_attn_bwd_workspace_bytes(1, 2, 8192, 128) < 64 << 20
 
     def fwd(ptrs=None, T=300, D=64, sinks=4, m=None, lay=None):
         p = [FAKE] * 5 if ptrs is None else ptrs
@@ -256,7 +279,8 @@ def test_without_sinks_or_window_it_is_the_plain_call(D):
 
 
 @pytest.mark.gpu
-def test_fused_projection_and_autograd():
+@pytest.mark.parametrize("docs", [False, True])
+def test_fused_projection_and_autograd(docs):
     """q, k, v out of one projection, O and gradients token-major, through gpt_attention."""
     gpu()
     from causal_attention_sdpa_b200.autograd import gpt_attention
@@ -264,11 +288,11 @@ def test_fused_projection_and_autograd():
     g = torch.Generator().manual_seed(4)
     x = torch.randn(B, T, 3, H, D, generator=g).bfloat16()
     do = torch.randn(B, T, H, D, generator=g).bfloat16()
-    ds = np.array([[0] * 250 + [250] * 350, [0] * 600])
+    ds = np.array([[0] * 250 + [250] * 350, [0] * 600]) if docs else None
     leaf = x.cuda().requires_grad_()
     q, k, v = leaf.permute(2, 0, 3, 1, 4).unbind(0)
     o = gpt_attention(q, k, v, window=W, sinks=S, out_layout="bthd",
-                      doc_start=torch.as_tensor(ds, dtype=torch.int32).cuda())
+                      doc_start=torch.as_tensor(ds, dtype=torch.int32).cuda() if docs else None)
     o.backward(do.cuda())
     qh, kh, vh = x.permute(2, 0, 3, 1, 4).unbind(0)
     ro, _, *rg = streaming.attn_sinks(qh, kh, vh, D ** -0.5, W, S, ds, do.transpose(1, 2))
