@@ -1090,8 +1090,8 @@ int gpt_attn_pages_copy(void* k_pages, void* v_pages, int n_pages, int Hkv, int 
     p.n_pages = n_pages;
     p.page_chunks = Hkv * page * (D / 8);
     p.units = (p.page_chunks + kCopyUnit - 1) / kCopyUnit;
-    const long long most = 2LL * n_max * p.units, resident = 8LL * sm_count();
-    pages_copy_kernel<<<(unsigned)(most < resident ? most : resident), kCopyThreads, 0,
+    const long long most = 2LL * n_max * p.units, blocks = (long long)kCopyBlocksPerSm * sm_count();
+    pages_copy_kernel<<<(unsigned)(most < blocks ? most : blocks), kCopyThreads, 0,
                         static_cast<cudaStream_t>(stream)>>>(p);
     return cudaGetLastError() == cudaSuccess ? GPT_ATTN_OK : GPT_ATTN_ERR_CUDA;
 }

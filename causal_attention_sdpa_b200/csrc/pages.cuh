@@ -119,11 +119,15 @@ struct CopyParams {
 };
 
 constexpr int kCopyThreads = 256;
-constexpr int kCopyDeep = 4;                               // loads in flight per thread
-constexpr int kCopyUnit = kCopyThreads * kCopyDeep;        // 16 KB
+constexpr int kCopyDeep = 8;                               // loads in flight per thread
+constexpr int kCopyUnit = kCopyThreads * kCopyDeep;        // 32 KB
+constexpr int kCopyBlocksPerSm = 32;
 
-// Pages are cut into units of 16 KB; resident blocks take unit after unit, so a few large pages and
-// many small ones fill the GPU alike, and a count known only on the device costs nothing.
+// Bound by HBM.  Pages are cut into units of 32 KB and blocks take unit after unit, so a few large pages
+// and many small ones fill the GPU alike, and a count known only on the device costs little.  Packing
+// two pools of 0.5 GB of which half is in use (531 MB read and written) on one B200: 84 us, 6.3 TB/s, of a measured copy's
+// 6.5; with 4 loads a thread 94, with as many blocks as are resident (8 to an SM) 88, where the slowest
+// block's last unit is waited for.
 __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const __grid_constant__ CopyParams p) {
     const int n = p.n_pairs ? clamp_int(__ldg(p.n_pairs), 0, p.max_pairs) : p.max_pairs;
     const long long total = 2LL * n * p.units;

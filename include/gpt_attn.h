@@ -187,7 +187,8 @@ int gpt_attn_bwd_ex(const void* q, const void* k, const void* v, const void* o,
  * Everything else, layouts, ownership and errors, is as for those two; o and
  * lse of the backward pass come from gpt_attn_fwd_sinks with the same mask and
  * sinks, and its workspace has gpt_attn_bwd_sinks_workspace_bytes bytes
- * (window: the largest of the call's windows; 0 for shapes the pass rejects).
+ * (window: the largest of the call's windows; 0 for shapes the pass rejects),
+ * which with few heads and long rows is more than the plain pass needs.
  * The form for new tokens against a cache is gpt_attn_paged_decode.
  */
 int gpt_attn_fwd_sinks(const void* q, const void* k, const void* v, void* o, float* lse,
@@ -338,7 +339,7 @@ int gpt_attn_paged_append(const gpt_attn_paged_cache* cache, const void* k_new, 
  *   parents : const int32 [B, N] or NULL.
  *   workspace: >= gpt_attn_paged_decode_workspace_bytes(B, H, Hkv, N, D) bytes
  *             (0 for shapes the call rejects), 16-byte aligned, contents
- *             ignored on entry.
+ *             ignored on entry.  Calls that overlap on the GPU need one each.
  * What a node does not see does not reach it, infinities and NaN included.
  * Memory-bound up to some hundred rows N * H / Hkv per key head.  Errors as for
  * gpt_attn_decode.  Asynchronous on `stream`.
@@ -369,7 +370,7 @@ int gpt_attn_paged_accept(const gpt_attn_paged_cache* cache, const int* accepted
  * negative status is left as it was.  S, M, P >= 1 and S * M < 2^31.
  * Asynchronous on `stream`; the workspace of reserve, fork and compact has
  * gpt_attn_pages_workspace_bytes(S, M, P) bytes, 16-byte aligned, contents
- * ignored on entry.
+ * ignored on entry; calls that overlap on the GPU need one each.
  *
  * gpt_attn_pages_reserve: pages for tokens[s] more tokens than lens[s] (<= 0:
  *   nothing asked), behind those that the slot has.  -1 where M pages do not

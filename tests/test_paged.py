@@ -244,6 +244,10 @@ CASES = [
     (40, 8, 1, 64, 1, 16, [(37 * i) % 211 for i in range(40)], 0, 0, False),
     (300, 1, 1, 64, 1, 16, [(53 * i) % 97 for i in range(300)], 0, 0, False),
     (33, 3, 2, 128, 4, 32, [(91 * i) % 400 for i in range(33)], 30, 2, True),
+    (900, 1, 1, 64, 1, 16, [(29 * i) % 61 for i in range(900)], 0, 0, False),
+    (600, 1, 40, 64, 1, 8, [(29 * i) % 61 for i in range(600)], 20, 1, False),
+    (3, 1, 65, 128, 1, 16, [200, 64, 1], 0, 0, False), (2, 2, 5, 64, 26, 24, [400, 130], 60, 3, True),
+    (2, 1, 43, 128, 3, 1, [70, 5], 0, 0, True), (1, 2, 11, 64, 64, 2, [77], 0, 0, True),
 ]
 
 
@@ -375,10 +379,28 @@ def test_what_a_node_does_not_see_does_not_reach_it(D, G, N):
 
 
 @pytest.mark.gpu
-def test_append_decode_accept_as_a_user_runs_them():
+@pytest.mark.parametrize("G,N", [(1, 1), (2, 9), (9, 5), (3, 50)])
+def test_nothing_new_and_nothing_cached(G, N):
+    gpu()
+    k, v, table, ln = make_cache(3, 2, 64, 16, [0, 40, 7], N, seed=2)
+    q = torch.randn(3, 2 * G, N, 64).bfloat16()
+    a = cuda(q, k, v, table, ln)
+    nan = lambda: dict(o=torch.full_like(a[0], float("nan")), lse=torch.full((3, 2 * G, N), float("nan"), device="cuda"))
+    for n_new in ([0, 0, 0], [-1, 0, -2 ** 31], [0, min(N, 2), 0]):
+        o, lse = ga.gpt_attn_paged_decode(*a, n_new=torch.tensor(n_new, dtype=torch.int32, device="cuda"), **nan())
+        ro, rl = streaming.paged_decode(q, k, v, table, ln, None, n_new, 0.125)
+        close(o, lse, ro, rl)
+    t = torch.full_like(a[3], -1)                                   # no page anywhere
+    o, lse = ga.gpt_attn_paged_decode(*a[:3], t, a[4], **nan())
+    assert (o == 0).all() and torch.isneginf(lse).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("G", [2, 7])
+def test_append_decode_accept_as_a_user_runs_them(G):
     """A speculative loop over strided projections and a captured graph, against dense causal attention."""
     gpu()
-    B, Hkv, G, D, page, N = 3, 2, 2, 64, 16, 5
+    B, Hkv, D, page, N = 3, 2, 64, 16, 5
     H, M = Hkv * G, 12
     g = torch.Generator().manual_seed(1)
     P = B * M + 2
