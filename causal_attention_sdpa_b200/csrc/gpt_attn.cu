@@ -375,6 +375,39 @@ int launch_bwd_delta(const void* o, const float* lse, const void* dout, int B, i
     return cudaGetLastError() == cudaSuccess ? GPT_ATTN_OK : GPT_ATTN_ERR_CUDA;
 }
 
+// Delta from the keys for the rows that see few: the first ones of each document, hence without documents
+// of each head, unless a window with its sinks is as short as that.
+int launch_exact_delta(const void* q, const void* k, const void* v, const void* dout, int B, int H, int T, int D,
+                       float scale, void* ws, const SinkMask& mask, const Layout& L, cudaStream_t st) {
+    const WsLayout w = ws_layout(ws, B * H, T, D);
+    bool few = mask.doc_start != nullptr;
+    for (int h = 0; h < (mask.head_windows ? H : 1); ++h) {
+        const int W = mask.head_windows ? mask.win[h] : mask.window;
+        few |= W > 0 && (long long)W + mask.sinks <= kExactDelta;
+    }
+    DeltaKeys p;
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.k = static_cast<const __nv_bfloat16*>(k);
+    p.v = static_cast<const __nv_bfloat16*>(v);
+    p.d_o = static_cast<const __nv_bfloat16*>(dout);
+    p.q_str = L.q;
+    p.k_str = L.k;
+    p.v_str = L.v;
+    p.do_str = L.dO;
+    p.delta = w.delta;
+    p.lse2 = w.lse2;
+    p.BH = B * H;
+    p.H = H;
+    p.T = T;
+    p.T_pad = w.T_pad;
+    p.rows = few || T < kExactDelta ? T : kExactDelta;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    const unsigned grid = (unsigned)(((long long)p.BH * p.rows + 7) / 8);
+    if (D == 64) attn_exact_delta_kernel<64><<<grid, 256, 0, st>>>(p, mask);
+    else attn_exact_delta_kernel<128><<<grid, 256, 0, st>>>(p, mask);
+    return cudaGetLastError() == cudaSuccess ? GPT_ATTN_OK : GPT_ATTN_ERR_CUDA;
+}
+
 template <int D>
 int launch_bwd_grads(const void* q, const void* k, const void* v, const void* dout, void* dk, void* dv, int B,
                      int H, int T, float scale, const MaskParams& mask, const Layout& L, void* ws, cudaStream_t st,
@@ -827,8 +860,12 @@ int gpt_attn_bwd_sinks(const void* q, const void* k, const void* v, const void* 
         if (cut.most > 1 && workspace_bytes < sink_part_at(B * H, T, D) + sink_part_bytes_of(cut, B * H, D))
             return GPT_ATTN_ERR_WORKSPACE;
     }
-    sc = sp ? launch_bwd_delta(o, lse, dO, B, H, T, D, workspace, *sp, L, st)
-            : launch_bwd_delta(o, lse, dO, B, H, T, D, workspace, m, L, st);
+    if (sinks > 0) {
+        sc = launch_bwd_delta(o, lse, dO, B, H, T, D, workspace, sm, L, st);
+        if (sc == GPT_ATTN_OK) sc = launch_exact_delta(q, k, v, dO, B, H, T, D, scale, workspace, sm, L, st);
+    } else {
+        sc = launch_bwd_delta(o, lse, dO, B, H, T, D, workspace, m, L, st);
+    }
     if (sc != GPT_ATTN_OK) return sc;
     sc = D == 64 ? launch_bwd_grads<64>(q, k, v, dO, dk, dv, B, H, T, scale, m, L, workspace, st, sp)
                  : launch_bwd_grads<128>(q, k, v, dO, dk, dv, B, H, T, scale, m, L, workspace, st, sp);
