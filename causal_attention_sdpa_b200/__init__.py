@@ -386,6 +386,17 @@ def _launch(what, dev, stream, *args):
         raise GptAttnError(rc, what)
 
 
+def _keep(stream, *tensors):
+    """Memory taken here for a call on another stream than the current one: not to be handed out again
+    before the call has ended there."""
+    if stream is None:
+        return
+    if not hasattr(stream, "cuda_stream"):
+        stream = _t().cuda.ExternalStream(int(stream), device=tensors[0].device)
+    for t in tensors:
+        t.record_stream(stream)
+
+
 def _check_tensor(name, t, dtype, shape, dev):
     """A contiguous tensor of the given type and shape on CUDA device number `dev`."""
     if t.dtype is not dtype or t.get_device() != dev or dev < 0 or t.shape != shape or not t.is_contiguous():
@@ -437,7 +448,7 @@ def gpt_attn_fwd_sinks(q, k, v, window=0, sinks=0, scale=None, head_windows=None
     B, H, T, D, shape, dev = _check_sinks_call(q, doc_start, head_windows, lse)
     _check_views(dev, shape, q=q, k=k, v=v)
     if o is None:
-        o = torch.empty(shape, dtype=q.dtype, device=q.device)
+        o = torch.empty_like(q) if q.is_contiguous() else torch.empty(shape, dtype=q.dtype, device=q.device)
     else:
         _check_views(dev, shape, o=o)
     if lse is None:
@@ -448,6 +459,7 @@ def gpt_attn_fwd_sinks(q, k, v, window=0, sinks=0, scale=None, head_windows=None
         lay = _layout(q=q, k=k, v=v, o=o, dO=o, dq=o, dk=o, dv=o)
     _launch("gpt_attn_fwd_sinks", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), B,
             H, T, D, D ** -0.5 if scale is None else float(scale), ctypes.byref(m), int(sinks), _byref(lay))
+    _keep(stream, o, lse)
     return o, lse
 
 
@@ -480,6 +492,7 @@ def gpt_attn_bwd_sinks(q, k, v, o, lse, dO, window=0, sinks=0, scale=None, head_
             dO.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, H, T, D,
             D ** -0.5 if scale is None else float(scale), ctypes.byref(m), int(sinks), _byref(lay), workspace.data_ptr(),
             workspace.numel() * workspace.element_size())
+    _keep(stream, dq, dk, dv, workspace)
     return dq, dk, dv
 
 
@@ -622,7 +635,7 @@ def gpt_attn_paged_decode(q, k_pages, v_pages, table, lens, parents=None, n_new=
     B = cache.B
     _check_views(dev, (B, H, N, cache.D), q=q)
     if o is None:
-        o = torch.empty(shape, dtype=q.dtype, device=device)
+        o = torch.empty_like(q) if q.is_contiguous() else torch.empty(shape, dtype=q.dtype, device=device)
     else:
         _check_views(dev, shape, o=o)
     if lse is None:
@@ -641,6 +654,7 @@ def gpt_attn_paged_decode(q, k_pages, v_pages, table, lens, parents=None, n_new=
     _launch("gpt_attn_paged_decode", dev, stream, q.data_ptr(), ctypes.byref(cache), _ptr(n_new), _ptr(parents),
             o.data_ptr(), lse.data_ptr(), H, N, D ** -0.5 if scale is None else float(scale), int(window), int(sinks),
             _pair_strides(q, o), workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    _keep(stream, o, lse, workspace)
     return o, lse
 
 
@@ -683,6 +697,8 @@ def _pages_workspace(workspace, S, M, P, table):
 def _int32_out(name, t, shape, like):
     """An int32 result of the given shape: the caller's, checked, or a new one on the device of `like`."""
     if t is None:
+        if like.shape == shape:
+            return _t().empty_like(like)
         return _t().empty(shape, dtype=_t().int32, device=like.device)
     _check_int32(name, t, shape, like.get_device())
     return t
@@ -694,10 +710,11 @@ def gpt_attn_pages_reserve(table, lens, refs, page, tokens, status=None, workspa
     row is too short), -2 not enough free pages."""
     S, M, P, dev = _check_state(table, refs, lens)
     _check_int32("tokens", tokens, (S,), dev)
-    status = _int32_out("status", status, (S,), table)
+    status = _int32_out("status", status, (S,), tokens)
     ws = _pages_workspace(workspace, S, M, P, table)
     _launch("gpt_attn_pages_reserve", dev, stream, table.data_ptr(), lens.data_ptr(), refs.data_ptr(), S, M, P, int(page),
             tokens.data_ptr(), status.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
+    _keep(stream, status, ws)
     return status
 
 
@@ -708,11 +725,12 @@ def gpt_attn_pages_fork(table, lens, refs, page, parents, status=None, pairs=Non
     with gpt_attn_pages_copy in every layer's pools."""
     S, M, P, dev = _check_state(table, refs, lens)
     _check_int32("parents", parents, (S,), dev)
-    status = _int32_out("status", status, (S,), table)
+    status = _int32_out("status", status, (S,), parents)
     pairs = _int32_out("pairs", pairs, (S, 2), table)
     ws = _pages_workspace(workspace, S, M, P, table)
     _launch("gpt_attn_pages_fork", dev, stream, table.data_ptr(), lens.data_ptr(), refs.data_ptr(), S, M, P, int(page),
             parents.data_ptr(), status.data_ptr(), pairs.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
+    _keep(stream, status, pairs, ws)
     return status, pairs
 
 
@@ -734,6 +752,7 @@ def gpt_attn_pages_compact(table, refs, workspace=None, stream=None):
     ws = _pages_workspace(workspace, S, M, P, table)
     _launch("gpt_attn_pages_compact", dev, stream, table.data_ptr(), refs.data_ptr(), S, M, P, new_table.data_ptr(),
             new_refs.data_ptr(), pairs.data_ptr(), moves.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
+    _keep(stream, results, ws)
     return new_table, new_refs, pairs, moves
 
 

@@ -457,6 +457,36 @@ def test_append_decode_accept_as_a_user_runs_them(G):
 
 
 @pytest.mark.gpu
+def test_memory_taken_for_a_call_on_another_stream_is_kept():
+    """Outputs and workspaces that the binding allocates are not handed out again while the call waits on
+    its own stream."""
+    gpu()
+    k, v, table, ln = make_cache(1, 2, 128, 64, [6000], 40, seed=5)
+    q = torch.randn(1, 2, 40, 128, generator=torch.Generator().manual_seed(3)).bfloat16()
+    a = cuda(q, k, v, table, ln)
+    x = torch.randn(1, 2, 2000, 128, device="cuda").bfloat16()
+    o0, lse0 = ga.gpt_attn_paged_decode(*a)
+    f0, l0 = ga.gpt_attn_fwd_sinks(x, x, x, window=100, sinks=4)
+    want = [o0.clone(), ga.gpt_attn_bwd_sinks(x, x, x, f0, l0, x, window=100, sinks=4)[2].clone()]
+    torch.cuda.synchronize()
+    for raw in (False, True):
+        s = torch.cuda.Stream()
+        arg = s.cuda_stream if raw else s
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(20_000_000)                           # some 10 ms before the calls run
+        got = []
+        for _ in range(4):
+            o, lse = ga.gpt_attn_paged_decode(*a, stream=arg)
+            dv = ga.gpt_attn_bwd_sinks(x, x, x, f0, l0, x, window=100, sinks=4, stream=arg)[2]
+            got.append((o, dv))
+            for n in (2 ** 12, 2 ** 16, 2 ** 20, 2 ** 22, 2 ** 24):  # the current stream overwrites what it gets
+                torch.full((n,), float("nan"), device="cuda")
+        torch.cuda.synchronize()
+        for o, dv in got:
+            assert torch.equal(o, want[0]) and torch.equal(dv, want[1])
+
+
+@pytest.mark.gpu
 def test_accept_any_order_and_repeats():
     gpu()
     k, v, table, ln = make_cache(2, 3, 128, 16, [30, 5], 64, seed=5)
