@@ -457,6 +457,35 @@ def test_append_decode_accept_as_a_user_runs_them(G):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("N", [2, 40])
+def test_pools_past_four_gigabytes(N):
+    """The same sequences in a small pool and at the far end of one of 4.4 GB: equal results."""
+    gpu()
+    Hkv, D, page, far = 8, 128, 64, 33500
+    k, v, table, ln = make_cache(2, Hkv, D, page, [200, 70], N, seed=5)
+    P = k.shape[0]
+    q = torch.randn(2, Hkv, N, D, generator=torch.Generator().manual_seed(3)).bfloat16()
+    qd, kd, vd, td, ld = cuda(q, k, v, table, ln)
+    kn = torch.randn(2, Hkv, N, D, device="cuda").bfloat16()
+    acc = torch.tensor([[N - 1] + [0] * (N - 1), list(range(N - 1, -1, -1))], dtype=torch.int32, device="cuda")
+    n_acc = torch.tensor([1, N], dtype=torch.int32, device="cuda")
+    kb, vb = (torch.empty(far, Hkv, page, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    assert kb.numel() * 2 > 2 ** 32
+    kb[far - P:], vb[far - P:] = kd, vd
+    tb = torch.where(td >= 0, td + far - P, td)
+    pairs = torch.tensor([[0, P - 1]], dtype=torch.int32, device="cuda")
+    got = []
+    for kk, vv, tt, off in ((kd, vd, td, 0), (kb, vb, tb, far - P)):
+        ga.gpt_attn_paged_append(kk, vv, tt, ld, kn, kn)
+        got.append(list(ga.gpt_attn_paged_decode(qd, kk, vv, tt, ld)))
+        ga.gpt_attn_paged_accept(kk, vv, tt, ld, acc, n_acc)
+        ga.gpt_attn_pages_copy(kk, vv, pairs + off)
+        got[-1] += [kk[off:].nan_to_num(9), vv[off:].nan_to_num(9)]
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
 def test_memory_taken_for_a_call_on_another_stream_is_kept():
     """Outputs and workspaces that the binding allocates are not handed out again while the call waits on
     its own stream."""
