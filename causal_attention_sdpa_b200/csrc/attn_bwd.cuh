@@ -160,6 +160,88 @@ struct BwdSmem {
     int abort_flag;
 };
 
+// With sinks, rows that see up to kExactDelta keys get Delta_i = sum_j P_ij dP_ij from the keys instead:
+// dO_i . O_i takes over the rounding of O to bf16, which weighs most where dS is small against P dP, that
+// is where a row sees few keys.  At T=37 with all keys in reach dQ and dK come from 0.00276 to 0.00241 of exact
+// (relative norm, of which 0.0024 are their own rounding and that of dS), at T=512, window 8, 4 sinks from
+// 0.00263 to 0.00235.  A warp to a row, D / 8 lanes to a key; of each head the first `rows` rows are looked at.
+// In the prep kernel, whose registers it doubled, this cost 13 us of 115 at B=8 H=12 T=1024 D=64; in a kernel
+// of its own 3; launched so that it runs beside the prep kernel, which leaves these rows out, 2.
+constexpr int kExactDelta = 16;
+struct DeltaKeys {
+    const __nv_bfloat16 *q, *k, *v, *d_o;
+    Strides q_str, k_str, v_str, do_str;
+    float* delta;                 // [BH, T_pad]
+    const float* lse;             // [BH, T]
+    int BH, H, T, T_pad, rows;
+    float scale_log2;
+};
+
+// Keys that query t sees: ns sinks from d on, then its window from lo on.
+struct SinkKeys {
+    int d, ns, lo, n;
+};
+__device__ __forceinline__ SinkKeys sink_keys(const SinkMask& mask, int bh, int T, int t) {
+    SinkKeys k;
+    k.lo = mask.row_lower_of(bh, T, mask.head_window(bh), t);
+    k.d = mask.doc_of(bh, T, t);
+    k.ns = max(min(k.d + mask.sinks, k.lo) - k.d, 0);
+    k.n = k.ns + t - k.lo + 1;
+    return k;
+}
+
+template <int D>
+__device__ __forceinline__ void exact_delta(const DeltaKeys& p, const SinkMask& mask, long long row) {
+    constexpr int G = D / 8, kAtOnce = 32 / G;
+    const int lane = threadIdx.x & 31, g = lane % G, slot = lane / G;
+    const int bh = (int)(row / p.rows), t = (int)(row - (long long)bh * p.rows);
+    const SinkKeys seen = sink_keys(mask, bh, p.T, t);
+    const int n = seen.n;
+    if (n > kExactDelta) return;
+    const uint4 qw = *reinterpret_cast<const uint4*>(p.q + p.q_str.row(bh, p.H, t) + g * 8);
+    const uint4 dw = *reinterpret_cast<const uint4*>(p.d_o + p.do_str.row(bh, p.H, t) + g * 8);
+    uint4 kw[kExactDelta / kAtOnce], vw[kExactDelta / kAtOnce];
+#pragma unroll
+    for (int x = 0; x < kExactDelta / kAtOnce; ++x) {
+        const int i = min(x * kAtOnce + slot, n - 1), key = i < seen.ns ? seen.d + i : seen.lo + (i - seen.ns);
+        kw[x] = *reinterpret_cast<const uint4*>(p.k + p.k_str.row(bh, p.H, key) + g * 8);
+        vw[x] = *reinterpret_cast<const uint4*>(p.v + p.v_str.row(bh, p.H, key) + g * 8);
+    }
+    auto dot = [](const uint4& a, const uint4& b) {
+        const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+        float s = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 u = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&x[e]));
+            const float2 w = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&y[e]));
+            s = fmaf(u.x, w.x, fmaf(u.y, w.y, s));
+        }
+        return s;
+    };
+    const float lse2 = p.lse[(size_t)bh * p.T + t] * 1.4426950408889634f;
+    float sum = 0.f;
+#pragma unroll
+    for (int x = 0; x < kExactDelta / kAtOnce; ++x) {
+        float s = dot(qw, kw[x]), dp = dot(dw, vw[x]);
+#pragma unroll
+        for (int off = G / 2; off > 0; off >>= 1) {
+            s += __shfl_xor_sync(0xffffffffu, s, off);
+            dp += __shfl_xor_sync(0xffffffffu, dp, off);
+        }
+        if (x * kAtOnce + slot < n) sum = fmaf(ex2_approx(fmaf(s, p.scale_log2, -lse2)), dp, sum);
+    }
+#pragma unroll
+    for (int off = G; off < 32; off *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    if (lane == 0) p.delta[(size_t)bh * p.T_pad + t] = sum;
+}
+
+template <int D>
+__global__ void __launch_bounds__(256) attn_exact_delta_kernel(const DeltaKeys p, const SinkMask mask) {
+    const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (row < (long long)p.BH * p.rows) exact_delta<D>(p, mask, row);
+    wait_prerequisites();                            // the end of this kernel is the end of the prep kernel too
+}
+
 // Delta_i = dO_i . O_i, lse2_i = lse_i * log2(e) for every padded row, and a
 // zeroed fp32 dQ accumulator.  G = D / 8 threads per row, 16-byte accesses.
 // No thread leaves before the group shuffle (every lane of the warp takes part).
@@ -176,8 +258,10 @@ attn_bwd_prep_kernel(const __nv_bfloat16* __restrict__ o, const __nv_bfloat16* _
                      const float* __restrict__ lse, float* __restrict__ lse2, float* __restrict__ delta,
                      float* __restrict__ dq_acc, int* __restrict__ sched, int T, int T_pad,
                      long long total_rows_pad, const Mask mask, int* __restrict__ lower2,
-                     int* __restrict__ last_qt, int n_tiles, const Strides o_str, const Strides do_str, int H) {
+                     int* __restrict__ last_qt, int n_tiles, const Strides o_str, const Strides do_str, int H,
+                     int exact_rows) {
     constexpr int G = D / 8;
+    if constexpr (Mask::kSinks) launch_dependents();
     if (blockIdx.x == 0 && threadIdx.x == 0) *sched = 0;
     const long long row = (long long)blockIdx.x * (256 / G) + threadIdx.x / G;
     const int g = threadIdx.x % G;
@@ -206,7 +290,9 @@ attn_bwd_prep_kernel(const __nv_bfloat16* __restrict__ o, const __nv_bfloat16* _
 #pragma unroll
     for (int off = G / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
     if (in_range && g == 0) {
-        delta[row] = valid ? acc : 0.f;
+        bool exact = false;                          // attn_exact_delta_kernel writes this row's
+        if constexpr (Mask::kSinks) exact = valid && t < exact_rows && sink_keys(mask, (int)bh, T, t).n <= kExactDelta;
+        if (!exact) delta[row] = valid ? acc : 0.f;
         lse2[row] = valid ? lse[bh * T + t] * 1.4426950408889634f : INFINITY;
         if (lower2) {
             const int W = mask_window(mask, (int)bh);
@@ -226,69 +312,6 @@ attn_bwd_prep_kernel(const __nv_bfloat16* __restrict__ o, const __nv_bfloat16* _
             }
         }
     }
-}
-
-// With sinks, rows that see up to kExactDelta keys get Delta_i = sum_j P_ij dP_ij from the keys instead:
-// dO_i . O_i takes over the rounding of O to bf16, which weighs most where dS is small against P dP, that
-// is where a row sees few keys.  At T=37 with all keys in reach dQ and dK come from 0.00276 to 0.00241 of exact
-// (relative norm, of which 0.0024 are their own rounding and that of dS), at T=512, window 8, 4 sinks from
-// 0.00263 to 0.00235.  A warp to a row, D / 8 lanes to a key; of each head the first `rows` rows are looked at.
-// In the prep kernel, whose registers it doubled, this cost 13 us of 115 at B=8 H=12 T=1024 D=64; here 3.
-constexpr int kExactDelta = 16;
-struct DeltaKeys {
-    const __nv_bfloat16 *q, *k, *v, *d_o;
-    Strides q_str, k_str, v_str, do_str;
-    float* delta;                 // [BH, T_pad]
-    const float* lse2;            // [BH, T_pad]
-    int BH, H, T, T_pad, rows;
-    float scale_log2;
-};
-
-template <int D>
-__global__ void __launch_bounds__(256) attn_exact_delta_kernel(const DeltaKeys p, const SinkMask mask) {
-    constexpr int G = D / 8, kAtOnce = 32 / G;
-    const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (row >= (long long)p.BH * p.rows) return;
-    const int lane = threadIdx.x & 31, g = lane % G, slot = lane / G;
-    const int bh = (int)(row / p.rows), t = (int)(row - (long long)bh * p.rows);
-    const int W = mask.head_window(bh), lo = mask.row_lower_of(bh, p.T, W, t), d = mask.doc_of(bh, p.T, t);
-    const int ns = max(min(d + mask.sinks, lo) - d, 0), n = ns + t - lo + 1;
-    if (n > kExactDelta) return;
-    const uint4 qw = *reinterpret_cast<const uint4*>(p.q + p.q_str.row(bh, p.H, t) + g * 8);
-    const uint4 dw = *reinterpret_cast<const uint4*>(p.d_o + p.do_str.row(bh, p.H, t) + g * 8);
-    uint4 kw[kExactDelta / kAtOnce], vw[kExactDelta / kAtOnce];
-#pragma unroll
-    for (int x = 0; x < kExactDelta / kAtOnce; ++x) {
-        const int i = min(x * kAtOnce + slot, n - 1), key = i < ns ? d + i : lo + (i - ns);
-        kw[x] = *reinterpret_cast<const uint4*>(p.k + p.k_str.row(bh, p.H, key) + g * 8);
-        vw[x] = *reinterpret_cast<const uint4*>(p.v + p.v_str.row(bh, p.H, key) + g * 8);
-    }
-    auto dot = [](const uint4& a, const uint4& b) {
-        const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
-        float s = 0.f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float2 u = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&x[e]));
-            const float2 w = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&y[e]));
-            s = fmaf(u.x, w.x, fmaf(u.y, w.y, s));
-        }
-        return s;
-    };
-    const float lse2 = p.lse2[(size_t)bh * p.T_pad + t];
-    float sum = 0.f;
-#pragma unroll
-    for (int x = 0; x < kExactDelta / kAtOnce; ++x) {
-        float s = dot(qw, kw[x]), dp = dot(dw, vw[x]);
-#pragma unroll
-        for (int off = G / 2; off > 0; off >>= 1) {
-            s += __shfl_xor_sync(0xffffffffu, s, off);
-            dp += __shfl_xor_sync(0xffffffffu, dp, off);
-        }
-        if (x * kAtOnce + slot < n) sum = fmaf(ex2_approx(fmaf(s, p.scale_log2, -lse2)), dp, sum);
-    }
-#pragma unroll
-    for (int off = G; off < 32; off *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    if (lane == 0) p.delta[(size_t)bh * p.T_pad + t] = sum;
 }
 
 // dK and dV of the key tiles that were cut: the pieces' sums, added in order.  G = D / 8 threads to a row.

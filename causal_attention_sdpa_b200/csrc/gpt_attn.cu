@@ -355,7 +355,7 @@ int sm_count() {
 
 template <typename Mask>
 int launch_bwd_delta(const void* o, const float* lse, const void* dout, int B, int H, int T, int D, void* ws,
-                     const Mask& mask, const Layout& L, cudaStream_t st) {
+                     const Mask& mask, const Layout& L, cudaStream_t st, int exact_rows = 0) {
     const int BH = B * H;
     const WsLayout w = ws_layout(ws, BH, T, D);
     const long long rows = (long long)BH * w.T_pad;
@@ -367,24 +367,29 @@ int launch_bwd_delta(const void* o, const float* lse, const void* dout, int B, i
     if (D == 64)
         attn_bwd_prep_kernel<64, Mask><<<grid, 256, 0, st>>>(o16, do16, lse, w.lse2, w.delta, w.dq_acc, w.sched, T,
                                                              w.T_pad, rows, mask, doc ? w.lower2 : nullptr,
-                                                             w.last_qt, w.n_tiles, L.o, L.dO, H);
+                                                             w.last_qt, w.n_tiles, L.o, L.dO, H, exact_rows);
     else
         attn_bwd_prep_kernel<128, Mask><<<grid, 256, 0, st>>>(o16, do16, lse, w.lse2, w.delta, w.dq_acc, w.sched, T,
                                                               w.T_pad, rows, mask, doc ? w.lower2 : nullptr,
-                                                              w.last_qt, w.n_tiles, L.o, L.dO, H);
+                                                              w.last_qt, w.n_tiles, L.o, L.dO, H, exact_rows);
     return cudaGetLastError() == cudaSuccess ? GPT_ATTN_OK : GPT_ATTN_ERR_CUDA;
 }
 
-// Delta from the keys for the rows that see few: the first ones of each document, hence without documents
-// of each head, unless a window with its sinks is as short as that.
-int launch_exact_delta(const void* q, const void* k, const void* v, const void* dout, int B, int H, int T, int D,
-                       float scale, void* ws, const SinkMask& mask, const Layout& L, cudaStream_t st) {
-    const WsLayout w = ws_layout(ws, B * H, T, D);
+// Rows of each head among which there are some that see few keys: the first ones of each document, hence
+// without documents of the head, unless a window with its sinks is as short as that.
+int exact_delta_rows(const SinkMask& mask, int H, int T) {
     bool few = mask.doc_start != nullptr;
     for (int h = 0; h < (mask.head_windows ? H : 1); ++h) {
         const int W = mask.head_windows ? mask.win[h] : mask.window;
         few |= W > 0 && (long long)W + mask.sinks <= kExactDelta;
     }
+    return few || T < kExactDelta ? T : kExactDelta;
+}
+
+// Delta from the keys for those rows; the prep kernel before it has left them out.
+int launch_exact_delta(const void* q, const void* k, const void* v, const float* lse, const void* dout, int B, int H,
+                       int T, int D, float scale, void* ws, const SinkMask& mask, const Layout& L, cudaStream_t st) {
+    const WsLayout w = ws_layout(ws, B * H, T, D);
     DeltaKeys p;
     p.q = static_cast<const __nv_bfloat16*>(q);
     p.k = static_cast<const __nv_bfloat16*>(k);
@@ -395,17 +400,17 @@ int launch_exact_delta(const void* q, const void* k, const void* v, const void* 
     p.v_str = L.v;
     p.do_str = L.dO;
     p.delta = w.delta;
-    p.lse2 = w.lse2;
+    p.lse = lse;
     p.BH = B * H;
     p.H = H;
     p.T = T;
     p.T_pad = w.T_pad;
-    p.rows = few || T < kExactDelta ? T : kExactDelta;
+    p.rows = exact_delta_rows(mask, H, T);
     p.scale_log2 = scale * 1.4426950408889634f;
-    const unsigned grid = (unsigned)(((long long)p.BH * p.rows + 7) / 8);
-    if (D == 64) attn_exact_delta_kernel<64><<<grid, 256, 0, st>>>(p, mask);
-    else attn_exact_delta_kernel<128><<<grid, 256, 0, st>>>(p, mask);
-    return cudaGetLastError() == cudaSuccess ? GPT_ATTN_OK : GPT_ATTN_ERR_CUDA;
+    const dim3 grid((unsigned)(((long long)p.BH * p.rows + 7) / 8));
+    return launch_dependent(D == 64 ? attn_exact_delta_kernel<64> : attn_exact_delta_kernel<128>, grid, 256, 0, st, p, mask)
+               ? GPT_ATTN_OK
+               : GPT_ATTN_ERR_CUDA;
 }
 
 template <int D>
@@ -861,8 +866,8 @@ int gpt_attn_bwd_sinks(const void* q, const void* k, const void* v, const void* 
             return GPT_ATTN_ERR_WORKSPACE;
     }
     if (sinks > 0) {
-        sc = launch_bwd_delta(o, lse, dO, B, H, T, D, workspace, sm, L, st);
-        if (sc == GPT_ATTN_OK) sc = launch_exact_delta(q, k, v, dO, B, H, T, D, scale, workspace, sm, L, st);
+        sc = launch_bwd_delta(o, lse, dO, B, H, T, D, workspace, sm, L, st, exact_delta_rows(sm, H, T));
+        if (sc == GPT_ATTN_OK) sc = launch_exact_delta(q, k, v, lse, dO, B, H, T, D, scale, workspace, sm, L, st);
     } else {
         sc = launch_bwd_delta(o, lse, dO, B, H, T, D, workspace, m, L, st);
     }
