@@ -16,9 +16,12 @@ Entry points (same names as the C ABI, see include/gpt_attn.h):
   gpt_attn_check(stream=None) -> int
   gpt_attn_status_string(status) -> str
 Tensors are bf16 contiguous [B, H, T, D] on the GPU; lse is fp32 [B, H, T].
+`stream` (a torch stream or a raw handle) is where a call runs instead of on the current stream.  What the
+call allocates is taken there, and may be used on the current stream too once that waits for the other.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -386,15 +389,31 @@ def _launch(what, dev, stream, *args):
         raise GptAttnError(rc, what)
 
 
-def _keep(stream, *tensors):
-    """Memory taken here for a call on another stream than the current one: not to be handed out again
-    before the call has ended there."""
+_HERE = contextlib.nullcontext()
+
+
+def _memory_of(stream, dev):
+    """Context in which memory for a call on `stream` is taken: on that stream, so that what the call
+    writes comes after all that was done there with the memory before.  Work on the current stream
+    may still use what the allocator would hand out there, and nothing orders it and the call."""
+    if stream is None:
+        return _HERE
+    torch = _t()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream_handle(stream)
+        # 1 is another name of the legacy default stream, whose handle torch knows as 0
+        stream = torch.cuda.ExternalStream(0 if handle == 1 else handle, device=dev)
+    return torch.cuda.stream(stream)
+
+
+def _hand_over(stream, *tensors):
+    """Results of a call on another stream than the current one, whose memory came from there: not to be
+    handed out again before what the current stream does with them has ended."""
     if stream is None:
         return
-    if not hasattr(stream, "cuda_stream"):
-        stream = _t().cuda.ExternalStream(int(stream), device=tensors[0].device)
+    here = _t().cuda.current_stream(tensors[0].device)
     for t in tensors:
-        t.record_stream(stream)
+        t.record_stream(here)
 
 
 def _check_tensor(name, t, dtype, shape, dev):
@@ -447,19 +466,20 @@ def gpt_attn_fwd_sinks(q, k, v, window=0, sinks=0, scale=None, head_windows=None
     torch = _t()
     B, H, T, D, shape, dev = _check_sinks_call(q, doc_start, head_windows, lse)
     _check_views(dev, shape, q=q, k=k, v=v)
-    if o is None:
-        o = torch.empty_like(q) if q.is_contiguous() else torch.empty(shape, dtype=q.dtype, device=q.device)
-    else:
+    if o is not None:
         _check_views(dev, shape, o=o)
-    if lse is None:
-        lse = torch.empty((B, H, T), dtype=torch.float32, device=q.device)
+    with _memory_of(stream, dev):
+        if o is None:
+            o = torch.empty_like(q) if q.is_contiguous() else torch.empty(shape, dtype=q.dtype, device=q.device)
+        if lse is None:
+            lse = torch.empty((B, H, T), dtype=torch.float32, device=q.device)
     m, keep = _sinks_mask(H, window, head_windows, doc_start)
     lay = None
     if not (q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and o.is_contiguous()):
         lay = _layout(q=q, k=k, v=v, o=o, dO=o, dq=o, dk=o, dv=o)
     _launch("gpt_attn_fwd_sinks", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), B,
             H, T, D, D ** -0.5 if scale is None else float(scale), ctypes.byref(m), int(sinks), _byref(lay))
-    _keep(stream, o, lse)
+    _hand_over(stream, o, lse)
     return o, lse
 
 
@@ -475,24 +495,25 @@ def gpt_attn_bwd_sinks(q, k, v, o, lse, dO, window=0, sinks=0, scale=None, head_
     B, H, T, D, shape, dev = _check_sinks_call(q, doc_start, head_windows, lse)
     _check_views(dev, shape, q=q, k=k, v=v, o=o, dO=dO)
     device = q.device
-    if dq is None and dk is None and dv is None:
-        dq, dk, dv = torch.empty((3, B, H, T, D), dtype=q.dtype, device=device).unbind(0)     # one allocation
-    else:
-        dq, dk, dv = (torch.empty(shape, dtype=q.dtype, device=device) if t is None else t for t in (dq, dk, dv))
-        _check_views(dev, shape, dq=dq, dk=dk, dv=dv)
-    if workspace is None:
-        top = max(head_windows) if head_windows is not None else window
-        workspace = torch.empty(max(gpt_attn_bwd_sinks_workspace_bytes(B, H, T, D, top, sinks), 16),
-                                dtype=torch.uint8, device=device)
-    else:
+    if workspace is not None:
         _check_workspace(workspace, dev)
+    with _memory_of(stream, dev):
+        if dq is None and dk is None and dv is None:
+            dq, dk, dv = torch.empty((3, B, H, T, D), dtype=q.dtype, device=device).unbind(0)     # one allocation
+        else:
+            dq, dk, dv = (torch.empty(shape, dtype=q.dtype, device=device) if t is None else t for t in (dq, dk, dv))
+            _check_views(dev, shape, dq=dq, dk=dk, dv=dv)
+        if workspace is None:
+            top = max(head_windows) if head_windows is not None else window
+            workspace = torch.empty(max(gpt_attn_bwd_sinks_workspace_bytes(B, H, T, D, top, sinks), 16),
+                                    dtype=torch.uint8, device=device)
     m, keep = _sinks_mask(H, window, head_windows, doc_start)
     lay = _layout(q=q, k=k, v=v, o=o, dO=dO, dq=dq, dk=dk, dv=dv)
     _launch("gpt_attn_bwd_sinks", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
             dO.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, H, T, D,
             D ** -0.5 if scale is None else float(scale), ctypes.byref(m), int(sinks), _byref(lay), workspace.data_ptr(),
             workspace.numel() * workspace.element_size())
-    _keep(stream, dq, dk, dv, workspace)
+    _hand_over(stream, dq, dk, dv)
     return dq, dk, dv
 
 
@@ -634,27 +655,28 @@ def gpt_attn_paged_decode(q, k_pages, v_pages, table, lens, parents=None, n_new=
     _, H, N, D = shape
     B = cache.B
     _check_views(dev, (B, H, N, cache.D), q=q)
-    if o is None:
-        o = torch.empty_like(q) if q.is_contiguous() else torch.empty(shape, dtype=q.dtype, device=device)
-    else:
+    if o is not None:
         _check_views(dev, shape, o=o)
-    if lse is None:
-        lse = torch.empty((B, H, N), dtype=torch.float32, device=device)
-    else:
+    if lse is not None:
         _check_tensor("lse", lse, torch.float32, (B, H, N), dev)
     if parents is not None:
         _check_int32("parents", parents, (B, N), dev)
     if n_new is not None:
         _check_int32("n_new", n_new, (B,), dev)
-    if workspace is None:
-        need = gpt_attn_paged_decode_workspace_bytes(B, H, cache.Hkv, N, D)
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
-    else:
+    if workspace is not None:
         _check_workspace(workspace, dev)
+    with _memory_of(stream, dev):
+        if o is None:
+            o = torch.empty_like(q) if q.is_contiguous() else torch.empty(shape, dtype=q.dtype, device=device)
+        if lse is None:
+            lse = torch.empty((B, H, N), dtype=torch.float32, device=device)
+        if workspace is None:
+            need = gpt_attn_paged_decode_workspace_bytes(B, H, cache.Hkv, N, D)
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
     _launch("gpt_attn_paged_decode", dev, stream, q.data_ptr(), ctypes.byref(cache), _ptr(n_new), _ptr(parents),
             o.data_ptr(), lse.data_ptr(), H, N, D ** -0.5 if scale is None else float(scale), int(window), int(sinks),
             _pair_strides(q, o), workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    _keep(stream, o, lse, workspace)
+    _hand_over(stream, o, lse)
     return o, lse
 
 
@@ -710,11 +732,12 @@ def gpt_attn_pages_reserve(table, lens, refs, page, tokens, status=None, workspa
     row is too short), -2 not enough free pages."""
     S, M, P, dev = _check_state(table, refs, lens)
     _check_int32("tokens", tokens, (S,), dev)
-    status = _int32_out("status", status, (S,), tokens)
-    ws = _pages_workspace(workspace, S, M, P, table)
+    with _memory_of(stream, dev):
+        status = _int32_out("status", status, (S,), tokens)
+        ws = _pages_workspace(workspace, S, M, P, table)
     _launch("gpt_attn_pages_reserve", dev, stream, table.data_ptr(), lens.data_ptr(), refs.data_ptr(), S, M, P, int(page),
             tokens.data_ptr(), status.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
-    _keep(stream, status, ws)
+    _hand_over(stream, status)
     return status
 
 
@@ -725,12 +748,13 @@ def gpt_attn_pages_fork(table, lens, refs, page, parents, status=None, pairs=Non
     with gpt_attn_pages_copy in every layer's pools."""
     S, M, P, dev = _check_state(table, refs, lens)
     _check_int32("parents", parents, (S,), dev)
-    status = _int32_out("status", status, (S,), parents)
-    pairs = _int32_out("pairs", pairs, (S, 2), table)
-    ws = _pages_workspace(workspace, S, M, P, table)
+    with _memory_of(stream, dev):
+        status = _int32_out("status", status, (S,), parents)
+        pairs = _int32_out("pairs", pairs, (S, 2), table)
+        ws = _pages_workspace(workspace, S, M, P, table)
     _launch("gpt_attn_pages_fork", dev, stream, table.data_ptr(), lens.data_ptr(), refs.data_ptr(), S, M, P, int(page),
             parents.data_ptr(), status.data_ptr(), pairs.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
-    _keep(stream, status, pairs, ws)
+    _hand_over(stream, status, pairs)
     return status, pairs
 
 
@@ -746,13 +770,14 @@ def gpt_attn_pages_compact(table, refs, workspace=None, stream=None):
     [P // 2, 2], moves int32 [1]); gpt_attn_pages_copy(k, v, pairs, n_pairs=moves) moves the pages."""
     S, M, P, dev = _check_state(table, refs)
     n = P // 2
-    results = _t().empty(2 * n + S * M + P + 1, dtype=_t().int32, device=table.device)        # one allocation
+    with _memory_of(stream, dev):
+        results = _t().empty(2 * n + S * M + P + 1, dtype=_t().int32, device=table.device)    # one allocation
+        ws = _pages_workspace(workspace, S, M, P, table)
     pairs, new_table, new_refs, moves = results.split((2 * n, S * M, P, 1))
     pairs, new_table = pairs.view(n, 2), new_table.view(S, M)
-    ws = _pages_workspace(workspace, S, M, P, table)
     _launch("gpt_attn_pages_compact", dev, stream, table.data_ptr(), refs.data_ptr(), S, M, P, new_table.data_ptr(),
             new_refs.data_ptr(), pairs.data_ptr(), moves.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
-    _keep(stream, results, ws)
+    _hand_over(stream, results)
     return new_table, new_refs, pairs, moves
 
 
