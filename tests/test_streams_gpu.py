@@ -90,6 +90,20 @@ def test_memory_comes_from_the_stream_of_the_call(inputs, taken, name, raw):
 
 
 @pytest.mark.parametrize("name", sorted(CALLS))
+def test_memory_of_a_call_is_not_handed_out_while_it_waits(inputs, taken, name):
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)                           # some 10 ms before the call would run
+    CALLS[name](inputs, s)                                      # results and workspace are dropped
+    mine = list(taken)
+    taken.clear()
+    held = [torch.empty(b - a, dtype=torch.uint8, device="cuda") for a, b in mine for _ in range(3)]
+    assert len(taken) == len(held) > 0 and not overlap(taken, mine)
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("name", sorted(CALLS))
 def test_results_in_use_on_the_current_stream_are_kept(inputs, taken, name):
     """A result that is dropped while the current stream still has to read it is not written by the next
     call on the other stream."""
