@@ -178,6 +178,33 @@ def _stream_handle(stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+_HERE = contextlib.nullcontext()
+
+
+def _memory_of(stream, dev):
+    """Context in which memory for a call on `stream` is taken: on that stream, so that what the call
+    writes comes after all that was done there with the memory before.  Work on the current stream
+    may still use what the allocator would hand out there, and nothing orders it and the call."""
+    if stream is None:
+        return _HERE
+    torch = _t()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream_handle(stream)
+        # 1 is another name of the legacy default stream, whose handle torch knows as 0
+        stream = torch.cuda.ExternalStream(0 if handle == 1 else handle, device=dev)
+    return torch.cuda.stream(stream)
+
+
+def _hand_over(stream, *tensors):
+    """Results of a call on another stream than the current one, whose memory came from there: not to be
+    handed out again before what the current stream does with them has ended."""
+    if stream is None:
+        return
+    here = _t().cuda.current_stream(tensors[0].device)
+    for t in tensors:
+        t.record_stream(here)
+
+
 def _ptr(t):
     # A plain int: the c_void_p argtypes convert it (and None to NULL) without a wrapper object.
     return t.data_ptr() if t is not None else None
@@ -197,15 +224,17 @@ def gpt_attn_fwd(q, k, v, scale=None, window=0, o=None, lse=None, stream=None):
         _check_bf16(n, t, q.shape)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    if o is None:
-        o = torch.empty_like(q)
-    if lse is None:
-        lse = torch.empty((B, H, T), dtype=torch.float32, device=q.device)
+    with _memory_of(stream, q.get_device()):
+        if o is None:
+            o = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty((B, H, T), dtype=torch.float32, device=q.device)
     _check_bf16("o", o, q.shape)
     rc = lib().gpt_attn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, H, T, D, float(scale),
                             int(window), _stream_handle(stream))
     if rc != GPT_ATTN_OK:
         raise GptAttnError(rc, "gpt_attn_fwd")
+    _hand_over(stream, o, lse)
     return o, lse
 
 
@@ -222,18 +251,20 @@ def gpt_attn_bwd(q, k, v, o, lse, dO, scale=None, window=0, dq=None, dk=None, dv
         _check_bf16(n, t, q.shape)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(q) if dk is None else dk
-    dv = torch.empty_like(q) if dv is None else dv
     need = gpt_attn_bwd_workspace_bytes(B, H, T, D)
-    if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    with _memory_of(stream, q.get_device()):
+        dq = torch.empty_like(q) if dq is None else dq
+        dk = torch.empty_like(q) if dk is None else dk
+        dv = torch.empty_like(q) if dv is None else dv
+        if workspace is None:
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
     ws_bytes = workspace.numel() * workspace.element_size()
     rc = lib().gpt_attn_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dO), _ptr(dq), _ptr(dk),
                             _ptr(dv), B, H, T, D, float(scale), int(window), _ptr(workspace), ws_bytes,
                             _stream_handle(stream))
     if rc != GPT_ATTN_OK:
         raise GptAttnError(rc, "gpt_attn_bwd")
+    _hand_over(stream, dq, dk, dv)
     return dq, dk, dv
 
 
@@ -250,13 +281,15 @@ def gpt_attn_bwd_noalloc(q, k, v, o, lse, dO, scale=None, window=0, dq=None, dk=
         _check_bf16(n, t, q.shape)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(q) if dk is None else dk
-    dv = torch.empty_like(q) if dv is None else dv
+    with _memory_of(stream, q.get_device()):
+        dq = torch.empty_like(q) if dq is None else dq
+        dk = torch.empty_like(q) if dk is None else dk
+        dv = torch.empty_like(q) if dv is None else dv
     rc = lib().gpt_attn_bwd_noalloc(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dO), _ptr(dq), _ptr(dk),
                                     _ptr(dv), B, H, T, D, float(scale), int(window), _stream_handle(stream))
     if rc != GPT_ATTN_OK:
         raise GptAttnError(rc, "gpt_attn_bwd_noalloc")
+    _hand_over(stream, dq, dk, dv)
     return dq, dk, dv
 
 
@@ -319,9 +352,10 @@ def gpt_attn_fwd_ex(q, k, v, scale=None, window=0, head_windows=None, doc_start=
     if doc_start is not None and tuple(doc_start.shape) != (B, T):
         raise ValueError(f"doc_start must have shape {(B, T)}")
     scale = 1.0 / math.sqrt(D) if scale is None else scale
-    o = torch.empty((B, H, T, D), dtype=q.dtype, device=q.device) if o is None else o
+    with _memory_of(stream, q.get_device()):
+        o = torch.empty((B, H, T, D), dtype=q.dtype, device=q.device) if o is None else o
+        lse = torch.empty((B, H, T), dtype=torch.float32, device=q.device) if lse is None else lse
     _check_view("o", o, q.shape)
-    lse = torch.empty((B, H, T), dtype=torch.float32, device=q.device) if lse is None else lse
     m, keep = _mask(H, window, head_windows, doc_start)
     lay = _layout(q=q, k=k, v=v, o=o, dO=o, dq=o, dk=o, dv=o)
     rc = lib().gpt_attn_fwd_ex(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, H, T, D, float(scale),
@@ -329,6 +363,7 @@ def gpt_attn_fwd_ex(q, k, v, scale=None, window=0, head_windows=None, doc_start=
     del keep
     if rc != GPT_ATTN_OK:
         raise GptAttnError(rc, "gpt_attn_fwd_ex")
+    _hand_over(stream, o, lse)
     return o, lse
 
 
@@ -344,12 +379,13 @@ def gpt_attn_bwd_ex(q, k, v, o, lse, dO, scale=None, window=0, head_windows=None
         raise ValueError(f"doc_start must have shape {(B, T)}")
     scale = 1.0 / math.sqrt(D) if scale is None else scale
     mk = lambda: torch.empty((B, H, T, D), dtype=q.dtype, device=q.device)
-    dq = mk() if dq is None else dq
-    dk = mk() if dk is None else dk
-    dv = mk() if dv is None else dv
+    with _memory_of(stream, q.get_device()):
+        dq = mk() if dq is None else dq
+        dk = mk() if dk is None else dk
+        dv = mk() if dv is None else dv
+        ws, nbytes = _ws(workspace, q)
     for n, t in (("dq", dq), ("dk", dk), ("dv", dv)):
         _check_view(n, t, q.shape)
-    ws, nbytes = _ws(workspace, q)
     m, keep = _mask(H, window, head_windows, doc_start)
     lay = _layout(q=q, k=k, v=v, o=o, dO=dO, dq=dq, dk=dk, dv=dv)
     rc = lib().gpt_attn_bwd_ex(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dO), _ptr(dq), _ptr(dk),
@@ -358,6 +394,7 @@ def gpt_attn_bwd_ex(q, k, v, o, lse, dO, scale=None, window=0, head_windows=None
     del keep
     if rc != GPT_ATTN_OK:
         raise GptAttnError(rc, "gpt_attn_bwd_ex")
+    _hand_over(stream, dq, dk, dv)
     return dq, dk, dv
 
 
@@ -387,33 +424,6 @@ def _launch(what, dev, stream, *args):
             rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream)
     if rc != GPT_ATTN_OK:
         raise GptAttnError(rc, what)
-
-
-_HERE = contextlib.nullcontext()
-
-
-def _memory_of(stream, dev):
-    """Context in which memory for a call on `stream` is taken: on that stream, so that what the call
-    writes comes after all that was done there with the memory before.  Work on the current stream
-    may still use what the allocator would hand out there, and nothing orders it and the call."""
-    if stream is None:
-        return _HERE
-    torch = _t()
-    if not isinstance(stream, torch.cuda.Stream):
-        handle = _stream_handle(stream)
-        # 1 is another name of the legacy default stream, whose handle torch knows as 0
-        stream = torch.cuda.ExternalStream(0 if handle == 1 else handle, device=dev)
-    return torch.cuda.stream(stream)
-
-
-def _hand_over(stream, *tensors):
-    """Results of a call on another stream than the current one, whose memory came from there: not to be
-    handed out again before what the current stream does with them has ended."""
-    if stream is None:
-        return
-    here = _t().cuda.current_stream(tensors[0].device)
-    for t in tensors:
-        t.record_stream(here)
 
 
 def _check_tensor(name, t, dtype, shape, dev):
@@ -529,11 +539,13 @@ def _ws(workspace, q):
 def gpt_attn_bwd_delta(o, lse, dO, workspace, stream=None):
     """Stage 1 of the backward pass (Delta, scaled lse, zeroed dQ accumulator)."""
     B, H, T, D = o.shape
-    ws, nbytes = _ws(workspace, o)
+    with _memory_of(stream, o.get_device()):
+        ws, nbytes = _ws(workspace, o)
     rc = lib().gpt_attn_bwd_delta(_ptr(o), _ptr(lse), _ptr(dO), B, H, T, D, _ptr(ws), nbytes,
                                   _stream_handle(stream))
     if rc != GPT_ATTN_OK:
         raise GptAttnError(rc, "gpt_attn_bwd_delta")
+    _hand_over(stream, ws)
     return ws
 
 
@@ -577,16 +589,18 @@ def gpt_attn_decode(q, k_cache, v_cache, seq_lens, scale=None, window=0, o=None,
     if seq_lens.dtype != torch.int32 or not seq_lens.is_cuda or tuple(seq_lens.shape) != (B,):
         raise ValueError("seq_lens must be a CUDA int32 tensor [B]")
     scale = 1.0 / math.sqrt(D) if scale is None else scale
-    o = torch.empty_like(q) if o is None else o
-    lse = torch.empty((B, H), dtype=torch.float32, device=q.device) if lse is None else lse
     need = gpt_attn_decode_workspace_bytes(B, H, T, D, window)
-    if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    with _memory_of(stream, q.get_device()):
+        o = torch.empty_like(q) if o is None else o
+        lse = torch.empty((B, H), dtype=torch.float32, device=q.device) if lse is None else lse
+        if workspace is None:
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
     rc = lib().gpt_attn_decode(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(seq_lens), _ptr(o), _ptr(lse), B, H,
                                T, D, float(scale), int(window), _ptr(workspace),
                                workspace.numel() * workspace.element_size(), _stream_handle(stream))
     if rc != GPT_ATTN_OK:
         raise GptAttnError(rc, "gpt_attn_decode")
+    _hand_over(stream, o, lse)
     return o, lse
 
 
@@ -801,8 +815,9 @@ def gpt_attn_qk_prologue_fwd(q_raw, k_raw, qk_norm=True, rope_base=10000.0, q_ou
     import torch
     B, H, T, D = q_raw.shape
     mk = lambda: torch.empty((B, H, T, D), dtype=torch.bfloat16, device=q_raw.device)
-    q_out = mk() if q_out is None else q_out
-    k_out = mk() if k_out is None else k_out
+    with _memory_of(stream, q_raw.get_device()):
+        q_out = mk() if q_out is None else q_out
+        k_out = mk() if k_out is None else k_out
     ts = [q_raw, k_raw, q_out, k_out]
     for n, t in zip(("q_raw", "k_raw", "q_out", "k_out"), ts):
         _check_view(n, t, q_raw.shape)
@@ -811,6 +826,7 @@ def gpt_attn_qk_prologue_fwd(q_raw, k_raw, qk_norm=True, rope_base=10000.0, q_ou
                                         arr, _stream_handle(stream))
     if rc != GPT_ATTN_OK:
         raise GptAttnError(rc, "gpt_attn_qk_prologue_fwd")
+    _hand_over(stream, q_out, k_out)
     return q_out, k_out
 
 
@@ -820,8 +836,9 @@ def gpt_attn_qk_prologue_bwd(q_raw, k_raw, dq_out, dk_out, qk_norm=True, rope_ba
     import torch
     B, H, T, D = q_raw.shape
     mk = lambda: torch.empty((B, H, T, D), dtype=torch.bfloat16, device=q_raw.device)
-    dq_raw = mk() if dq_raw is None else dq_raw
-    dk_raw = mk() if dk_raw is None else dk_raw
+    with _memory_of(stream, q_raw.get_device()):
+        dq_raw = mk() if dq_raw is None else dq_raw
+        dk_raw = mk() if dk_raw is None else dk_raw
     ts = [q_raw, k_raw, dq_out, dk_out, dq_raw, dk_raw]
     for n, t in zip(("q_raw", "k_raw", "dq_out", "dk_out", "dq_raw", "dk_raw"), ts):
         _check_view(n, t, q_raw.shape)
@@ -830,6 +847,7 @@ def gpt_attn_qk_prologue_bwd(q_raw, k_raw, dq_out, dk_out, qk_norm=True, rope_ba
                                         arr, _stream_handle(stream))
     if rc != GPT_ATTN_OK:
         raise GptAttnError(rc, "gpt_attn_qk_prologue_bwd")
+    _hand_over(stream, dq_raw, dk_raw)
     return dq_raw, dk_raw
 
 

@@ -27,8 +27,11 @@ def inputs():
              refs=refs.cuda(), lens=torch.tensor([50, 64, 33, 49, 59, 0], dtype=torch.int32).cuda(),
              more=torch.tensor([9, 1, 0, 40, 2, 0], dtype=torch.int32).cuda(),
              parents=torch.tensor([-1, -1, -1, -1, -1, 0], dtype=torch.int32).cuda(), page=page,
-             cached=torch.tensor([45, 59, 28, 44, 54, 0], dtype=torch.int32).cuda(), dq=rnd(1, 2, 900, 64))
+             cached=torch.tensor([45, 59, 28, 44, 54, 0], dtype=torch.int32).cuda(), dq=rnd(1, 2, 900, 64),
+             one=rnd(1, 2, 64), at=torch.tensor([733], dtype=torch.int32).cuda())
     s["o"], s["lse"] = ga.gpt_attn_fwd_sinks(s["x"], s["x"], s["x"], window=100, sinks=4)
+    s["xs"] = [s["x"]] * 3
+    s["causal"] = [s["x"]] * 3 + list(ga.gpt_attn_fwd(*s["xs"])) + [s["x"]]
     torch.cuda.synchronize()
     return s
 
@@ -47,6 +50,15 @@ CALLS = {
     "reserve": lambda s, st: (ga.gpt_attn_pages_reserve(s["table"], s["lens"], s["refs"], s["page"], s["more"], stream=st),),
     "fork": lambda s, st: ga.gpt_attn_pages_fork(s["table"], s["lens"], s["refs"], s["page"], s["parents"], stream=st),
     "compact": lambda s, st: ga.gpt_attn_pages_compact(s["table"], s["refs"], stream=st),
+    "fwd": lambda s, st: ga.gpt_attn_fwd(*s["xs"], stream=st),
+    "fwd_ex": lambda s, st: ga.gpt_attn_fwd_ex(*s["xs"], head_windows=[0, 70], stream=st),
+    "bwd": lambda s, st: ga.gpt_attn_bwd(*s["causal"], stream=st),
+    "bwd_ex": lambda s, st: ga.gpt_attn_bwd_ex(*s["causal"], stream=st),
+    "bwd_noalloc": lambda s, st: ga.gpt_attn_bwd_noalloc(*s["causal"], stream=st),
+    "delta": lambda s, st: (ga.gpt_attn_bwd_delta(s["o"], s["lse"], s["x"], None, stream=st),),
+    "cache_decode": lambda s, st: ga.gpt_attn_decode(s["one"], s["x"], s["x"], s["at"], stream=st),
+    "prologue": lambda s, st: ga.gpt_attn_qk_prologue_fwd(s["x"], s["x"], stream=st),
+    "prologue_bwd": lambda s, st: ga.gpt_attn_qk_prologue_bwd(*s["xs"], s["x"], stream=st),
 }
 
 
@@ -67,6 +79,12 @@ def taken(monkeypatch, inputs):
     watch("empty")
     watch("empty_like")
     monkeypatch.setattr(ga, "_launch", lambda *a: None)
+    real = ga.lib()
+
+    class Lib:
+        def __getattr__(self, name):
+            return getattr(real, name) if name.endswith("_bytes") else lambda *a: ga.GPT_ATTN_OK
+    monkeypatch.setattr(ga, "lib", Lib)
     return seen
 
 
@@ -124,7 +142,7 @@ def test_results_in_use_on_the_current_stream_are_kept(inputs, taken, name):
 
 
 @pytest.mark.parametrize("raw", [False, True])
-@pytest.mark.parametrize("name", sorted(CALLS))
+@pytest.mark.parametrize("name", sorted(set(CALLS) - {"delta"}))       # delta's workspace has parts that nobody writes
 def test_work_queued_on_the_current_stream_does_not_reach_the_call(inputs, name, raw):
     """The current stream is late with writing memory that was given back there; the call's stream is idle."""
     def run(st):
