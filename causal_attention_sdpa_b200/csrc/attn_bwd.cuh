@@ -58,7 +58,8 @@ struct BwdParams {
     int BH;
     int n_tiles;
     int tail;               // heads of the unit list's class-major tail (schedule.h)
-    float scale_log2;       // scale * log2(e)
+    float scale_log2;       // ScoreScale
+    uint32_t score_sign;
     float scale;
     uint64_t timeout_ns;
     int units;              // work units in all
@@ -174,7 +175,7 @@ struct DeltaKeys {
     float* delta;                 // [BH, T_pad]
     const float* lse;             // [BH, T]
     int BH, H, T, T_pad, rows;
-    float scale_log2;
+    float scale_log2;             // scale log2 e, of either sign: nothing is masked here
 };
 
 // Keys that query t sees: ns sinks from d on, then its window from lo on.
@@ -384,7 +385,8 @@ attn_bwd_serial_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
     constexpr int kTileBytes = C::kTileBytes;
     constexpr int kBoxes = D / 64;
     constexpr uint32_t kTmemCols = 512;
-    constexpr uint32_t kIdescSS = idesc_bf16_f32(128, 128, 0, 0);    // S^T, dP^T
+    constexpr uint32_t kIdescSS = idesc_bf16_f32(128, 128, 0, 0);    // dP^T
+    const uint32_t idesc_s = kIdescSS | p.score_sign;                // S^T
     constexpr uint32_t kIdescKxMN = idesc_bf16_f32(128, D, 0, 1);    // dV (A in TMEM), dK
     constexpr uint32_t kIdescMNxMN = idesc_bf16_f32(128, D, 1, 1);   // dQ
 
@@ -506,7 +508,7 @@ attn_bwd_serial_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
                         for (int kk = 0; kk < D / 16; ++kk) {
                             const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
                             mma_ss(tmem + C::kColS, sw128_desc(k_addr + off, 16, 1024),
-                                   sw128_desc(q_addr + off, 16, 1024), kIdescSS, kk > 0);
+                                   sw128_desc(q_addr + off, 16, 1024), idesc_s, kk > 0);
                         }
                         mma_commit(&sm.bar_s_full);
                     } else if (warp == 2) {

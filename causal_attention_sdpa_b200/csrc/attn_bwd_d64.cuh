@@ -114,7 +114,8 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     constexpr int kStages = C::kStages;
     constexpr int kTileBytes = C::kTileBytes;
     constexpr uint32_t kTmemCols = 512;
-    constexpr uint32_t kIdescSS = idesc_bf16_f32(128, 128, 0, 0);    // S^T = K Q^T, dP^T = V dO^T
+    constexpr uint32_t kIdescSS = idesc_bf16_f32(128, 128, 0, 0);    // dP^T = V dO^T
+    const uint32_t idesc_s = kIdescSS | p.score_sign;                // S^T = K Q^T
     constexpr uint32_t kIdescKxMN = idesc_bf16_f32(128, D, 0, 1);    // dV (A = P^T in TMEM), dK
     constexpr uint32_t kIdescMNxMN = idesc_bf16_f32(128, D, 1, 1);   // dQ
 
@@ -245,7 +246,7 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
 #pragma unroll 1
                         for (int kk = 0; kk < D / 16; ++kk)
                             mma_ss(tmem + C::kColS, sw128_desc(k_addr + kk * 32, 16, 1024),
-                                   sw128_desc(q_addr + kk * 32, 16, 1024), kIdescSS, kk > 0);
+                                   sw128_desc(q_addr + kk * 32, 16, 1024), idesc_s, kk > 0);
                         mma_commit(&sm.bar_s_full);
 #pragma unroll 1
                         for (int kk = 0; kk < D / 16; ++kk)

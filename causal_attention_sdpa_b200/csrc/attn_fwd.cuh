@@ -117,6 +117,15 @@ struct Strides {
     }
 };
 
+// How the kernels take the scale of the scores: its magnitude goes into the exponents, its sign into the
+// product of queries and keys (the instruction descriptor's negation of an operand).  Masked scores are
+// -inf before the multiplication and row maxima are taken before it too, so it has to be above 0.  A scale of
+// 0 becomes the smallest normal number, which leaves every finite score's exponent at 0.
+struct ScoreScale {
+    float log2;           // |scale| log2 e
+    uint32_t sign;        // or-ed into the descriptor of the product
+};
+
 struct FwdParams {
     __nv_bfloat16* o;
     float* lse;
@@ -129,7 +138,8 @@ struct FwdParams {
     int tail;             // heads of the item list's class-major tail (schedule.h)
     int static_hpw;       // static order (schedule.h): heads per wave, and
     int static_waves;     // waves (0: items taken from the list through cluster launch control)
-    float scale_log2;     // scale * log2(e)
+    float scale_log2;     // ScoreScale
+    uint32_t score_sign;
     uint64_t timeout_ns;
 };
 
@@ -237,7 +247,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     constexpr int kTileBytes = C::kTileBytes;
     constexpr int kBoxes = D / 64;                 // 64-column TMA boxes per tile
     constexpr uint32_t kTmemCols = 512;
-    constexpr uint32_t kIdescQK = idesc_bf16_f32(128, 128, 0, 0);
+    const uint32_t idesc_qk = idesc_bf16_f32(128, 128, 0, 0) | p.score_sign;
     constexpr uint32_t kIdescPV = idesc_bf16_f32(128, D, 0, 1);
 
     const int warp = threadIdx.x >> 5;
@@ -429,7 +439,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                         for (int kk = 0; kk < D / 16; ++kk) {
                             const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
                             mma_ss(tmem + col, sw128_desc(q_addr + off, 16, 1024), sw128_desc(k_addr + off, 16, 1024),
-                                   kIdescQK, kk > 0);
+                                   idesc_qk, kk > 0);
                         }
                         mma_commit(&sm.bar_s_full[t]);
                         ++ct[t];

@@ -3,6 +3,7 @@
 // (except in gpt_attn_check, which exists to sync).
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 #include <stdlib.h>
@@ -237,6 +238,10 @@ MaskParams window_mask(int window, int H) {
     return m;
 }
 
+ScoreScale score_scale(float scale) {
+    return ScoreScale{scale == 0.f ? FLT_MIN : fabsf(scale) * 1.4426950408889634f, scale < 0.f ? kIdescNegateA : 0u};
+}
+
 template <int D>
 int launch_fwd(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H, int T, float scale,
                const MaskParams& mask, const Layout& L, cudaStream_t st, const SinkMask* sinks = nullptr) {
@@ -254,7 +259,9 @@ int launch_fwd(const void* q, const void* k, const void* v, void* o, float* lse,
     p.BH = BH;
     p.n_tiles = (T + kTile - 1) / kTile;
     p.n_blocks = (p.n_tiles + 1) / 2;
-    p.scale_log2 = scale * 1.4426950408889634f;
+    const ScoreScale ss = score_scale(scale);
+    p.scale_log2 = ss.log2;
+    p.score_sign = ss.sign;
     p.timeout_ns = wait_timeout_ns();
     // Work order (schedule.h): static waves with one block per SM when they make enough full
     // rotations (D = 64), else one block per item, the blocks that start taking the items of
@@ -444,7 +451,9 @@ int launch_bwd_grads(const void* q, const void* k, const void* v, const void* do
     p.tail = tail_heads(BH, std::max(1, w.n_tiles - p.cut.n_s), sm_count());
     p.lower2 = mask.doc_start ? w.lower2 : nullptr;
     p.last_qt = mask.doc_start ? w.last_qt : nullptr;
-    p.scale_log2 = scale * 1.4426950408889634f;
+    const ScoreScale ss = score_scale(scale);
+    p.scale_log2 = ss.log2;
+    p.score_sign = ss.sign;
     p.scale = scale;
     p.timeout_ns = wait_timeout_ns();
     const int units = p.units;

@@ -58,8 +58,9 @@ typedef enum {
  *   q, k, v : const bf16 [B, H, T, D], device.
  *   o       : bf16 [B, H, T, D], device, written.
  *   lse     : fp32 [B, H, T], device, written.
- *   scale   : multiplier of the scores; 1/sqrt(D) gives the softmax(QK^T/sqrt(d_k))
- *             of the definition (d_k read as the head dimension).
+ *   scale   : multiplier of the scores, any finite number (0: all visible keys weigh
+ *             the same); 1/sqrt(D) gives the softmax(QK^T/sqrt(d_k)) of the definition
+ *             (d_k read as the head dimension).
  *   window  : <= 0 causal; >= 1 sliding window of that many keys (diagonal included).
  * Returns GPT_ATTN_OK or an error code.  Asynchronous on `stream`.
  */
