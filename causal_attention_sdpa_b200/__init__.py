@@ -205,6 +205,19 @@ def _hand_over(stream, *tensors):
         t.record_stream(here)
 
 
+_INT_MAX = 2 ** 31 - 1
+
+
+def _reach(x):
+    """A window or a number of sinks as a C int: one past its range acts as its largest value does."""
+    return min(max(int(x), -_INT_MAX), _INT_MAX)
+
+
+def _fits(*sizes):
+    """Whether sizes are at least 1 and a C int holds them; ctypes would wrap others without a word."""
+    return min(sizes) >= 1 and max(sizes) <= _INT_MAX
+
+
 def _ptr(t):
     # A plain int: the c_void_p argtypes convert it (and None to NULL) without a wrapper object.
     return t.data_ptr() if t is not None else None
@@ -231,7 +244,7 @@ def gpt_attn_fwd(q, k, v, scale=None, window=0, o=None, lse=None, stream=None):
             lse = torch.empty((B, H, T), dtype=torch.float32, device=q.device)
     _check_bf16("o", o, q.shape)
     rc = lib().gpt_attn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, H, T, D, float(scale),
-                            int(window), _stream_handle(stream))
+                            _reach(window), _stream_handle(stream))
     if rc != GPT_ATTN_OK:
         raise GptAttnError(rc, "gpt_attn_fwd")
     _hand_over(stream, o, lse)
@@ -239,6 +252,8 @@ def gpt_attn_fwd(q, k, v, scale=None, window=0, o=None, lse=None, stream=None):
 
 
 def gpt_attn_bwd_workspace_bytes(B, H, T, D) -> int:
+    if not _fits(B, H, T, D):
+        return 0
     return int(lib().gpt_attn_bwd_workspace_bytes(int(B), int(H), int(T), int(D)))
 
 
@@ -260,7 +275,7 @@ def gpt_attn_bwd(q, k, v, o, lse, dO, scale=None, window=0, dq=None, dk=None, dv
             workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
     ws_bytes = workspace.numel() * workspace.element_size()
     rc = lib().gpt_attn_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dO), _ptr(dq), _ptr(dk),
-                            _ptr(dv), B, H, T, D, float(scale), int(window), _ptr(workspace), ws_bytes,
+                            _ptr(dv), B, H, T, D, float(scale), _reach(window), _ptr(workspace), ws_bytes,
                             _stream_handle(stream))
     if rc != GPT_ATTN_OK:
         raise GptAttnError(rc, "gpt_attn_bwd")
@@ -286,7 +301,7 @@ def gpt_attn_bwd_noalloc(q, k, v, o, lse, dO, scale=None, window=0, dq=None, dk=
         dk = torch.empty_like(q) if dk is None else dk
         dv = torch.empty_like(q) if dv is None else dv
     rc = lib().gpt_attn_bwd_noalloc(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dO), _ptr(dq), _ptr(dk),
-                                    _ptr(dv), B, H, T, D, float(scale), int(window), _stream_handle(stream))
+                                    _ptr(dv), B, H, T, D, float(scale), _reach(window), _stream_handle(stream))
     if rc != GPT_ATTN_OK:
         raise GptAttnError(rc, "gpt_attn_bwd_noalloc")
     _hand_over(stream, dq, dk, dv)
@@ -298,13 +313,13 @@ def _mask(H, window=0, head_windows=None, doc_start=None):
     import torch
     hw = None
     if head_windows is not None:
-        hw = (ctypes.c_int * H)(*[int(x) for x in head_windows])
+        hw = (ctypes.c_int * H)(*[_reach(x) for x in head_windows])
         if len(head_windows) != H:
             raise ValueError(f"head_windows needs {H} entries")
     if doc_start is not None:
         if doc_start.dtype != torch.int32 or not doc_start.is_cuda or not doc_start.is_contiguous():
             raise ValueError("doc_start must be a contiguous CUDA int32 tensor [B, T]")
-    m = GptAttnMask(int(window), ctypes.cast(hw, ctypes.POINTER(ctypes.c_int)) if hw is not None else None,
+    m = GptAttnMask(_reach(window), ctypes.cast(hw, ctypes.POINTER(ctypes.c_int)) if hw is not None else None,
                     doc_start.data_ptr() if doc_start is not None else None)
     return m, hw
 
@@ -465,7 +480,7 @@ def _check_sinks_call(q, doc_start, head_windows, lse):
 def _sinks_mask(H, window, head_windows, doc_start):
     if head_windows is not None:
         return _mask(H, window, head_windows, doc_start)
-    return GptAttnMask(int(window), None, None if doc_start is None else doc_start.data_ptr()), None
+    return GptAttnMask(_reach(window), None, None if doc_start is None else doc_start.data_ptr()), None
 
 
 def gpt_attn_fwd_sinks(q, k, v, window=0, sinks=0, scale=None, head_windows=None, doc_start=None, o=None, lse=None,
@@ -488,14 +503,17 @@ def gpt_attn_fwd_sinks(q, k, v, window=0, sinks=0, scale=None, head_windows=None
     if not (q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and o.is_contiguous()):
         lay = _layout(q=q, k=k, v=v, o=o, dO=o, dq=o, dk=o, dv=o)
     _launch("gpt_attn_fwd_sinks", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), B,
-            H, T, D, D ** -0.5 if scale is None else float(scale), ctypes.byref(m), int(sinks), _byref(lay))
+            H, T, D, D ** -0.5 if scale is None else float(scale), ctypes.byref(m), _reach(sinks), _byref(lay))
     _hand_over(stream, o, lse)
     return o, lse
 
 
 def gpt_attn_bwd_sinks_workspace_bytes(B, H, T, D, window=0, sinks=0) -> int:
     """Bytes of workspace of gpt_attn_bwd_sinks (window: the largest of the call's windows)."""
-    return int(lib().gpt_attn_bwd_sinks_workspace_bytes(int(B), int(H), int(T), int(D), int(window), int(sinks)))
+    if not _fits(B, H, T, D):
+        return 0
+    return int(lib().gpt_attn_bwd_sinks_workspace_bytes(int(B), int(H), int(T), int(D), _reach(window),
+                                                        _reach(sinks)))
 
 
 def gpt_attn_bwd_sinks(q, k, v, o, lse, dO, window=0, sinks=0, scale=None, head_windows=None, doc_start=None,
@@ -521,8 +539,8 @@ def gpt_attn_bwd_sinks(q, k, v, o, lse, dO, window=0, sinks=0, scale=None, head_
     lay = _layout(q=q, k=k, v=v, o=o, dO=dO, dq=dq, dk=dk, dv=dv)
     _launch("gpt_attn_bwd_sinks", dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
             dO.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, H, T, D,
-            D ** -0.5 if scale is None else float(scale), ctypes.byref(m), int(sinks), _byref(lay), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size())
+            D ** -0.5 if scale is None else float(scale), ctypes.byref(m), _reach(sinks), _byref(lay),
+            workspace.data_ptr(), workspace.numel() * workspace.element_size())
     _hand_over(stream, dq, dk, dv)
     return dq, dk, dv
 
@@ -556,7 +574,7 @@ def gpt_attn_bwd_grads(q, k, v, dO, dk, dv, workspace, scale=None, window=0, str
         scale = 1.0 / math.sqrt(D)
     ws, nbytes = _ws(workspace, q)
     rc = lib().gpt_attn_bwd_grads(_ptr(q), _ptr(k), _ptr(v), _ptr(dO), _ptr(dk), _ptr(dv), B, H, T, D,
-                                  float(scale), int(window), _ptr(ws), nbytes, _stream_handle(stream))
+                                  float(scale), _reach(window), _ptr(ws), nbytes, _stream_handle(stream))
     if rc != GPT_ATTN_OK:
         raise GptAttnError(rc, "gpt_attn_bwd_grads")
 
@@ -574,7 +592,9 @@ def gpt_attn_bwd_dq_convert(dq, workspace, scale=None, stream=None):
 
 
 def gpt_attn_decode_workspace_bytes(B, H, T_max, D, window=0) -> int:
-    return int(lib().gpt_attn_decode_workspace_bytes(int(B), int(H), int(T_max), int(D), int(window)))
+    if not _fits(B, H, T_max, D):
+        return 0
+    return int(lib().gpt_attn_decode_workspace_bytes(int(B), int(H), int(T_max), int(D), _reach(window)))
 
 
 def gpt_attn_decode(q, k_cache, v_cache, seq_lens, scale=None, window=0, o=None, lse=None, workspace=None,
@@ -596,7 +616,7 @@ def gpt_attn_decode(q, k_cache, v_cache, seq_lens, scale=None, window=0, o=None,
         if workspace is None:
             workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
     rc = lib().gpt_attn_decode(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(seq_lens), _ptr(o), _ptr(lse), B, H,
-                               T, D, float(scale), int(window), _ptr(workspace),
+                               T, D, float(scale), _reach(window), _ptr(workspace),
                                workspace.numel() * workspace.element_size(), _stream_handle(stream))
     if rc != GPT_ATTN_OK:
         raise GptAttnError(rc, "gpt_attn_decode")
@@ -652,6 +672,8 @@ def gpt_attn_paged_append(k_pages, v_pages, table, lens, k_new, v_new, n_new=Non
 
 
 def gpt_attn_paged_decode_workspace_bytes(B, H, Hkv, N, D) -> int:
+    if not _fits(B, H, Hkv, N, D):
+        return 0
     return int(lib().gpt_attn_paged_decode_workspace_bytes(int(B), int(H), int(Hkv), int(N), int(D)))
 
 
@@ -688,8 +710,8 @@ def gpt_attn_paged_decode(q, k_pages, v_pages, table, lens, parents=None, n_new=
             need = gpt_attn_paged_decode_workspace_bytes(B, H, cache.Hkv, N, D)
             workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
     _launch("gpt_attn_paged_decode", dev, stream, q.data_ptr(), ctypes.byref(cache), _ptr(n_new), _ptr(parents),
-            o.data_ptr(), lse.data_ptr(), H, N, D ** -0.5 if scale is None else float(scale), int(window), int(sinks),
-            _pair_strides(q, o), workspace.data_ptr(), workspace.numel() * workspace.element_size())
+            o.data_ptr(), lse.data_ptr(), H, N, D ** -0.5 if scale is None else float(scale), _reach(window),
+            _reach(sinks), _pair_strides(q, o), workspace.data_ptr(), workspace.numel() * workspace.element_size())
     _hand_over(stream, o, lse)
     return o, lse
 
@@ -701,12 +723,16 @@ def gpt_attn_paged_accept(k_pages, v_pages, table, lens, accepted, n_accepted, s
     if accepted.dim() != 2:
         raise ValueError("accepted must be a contiguous int32 tensor [B, N]")
     N = accepted.shape[1]
+    if N > _INT_MAX:
+        raise ValueError("accepted must have fewer than 2^31 columns")
     _check_int32("accepted", accepted, (cache.B, N), dev)
     _check_int32("n_accepted", n_accepted, (cache.B,), dev)
     _launch("gpt_attn_paged_accept", dev, stream, ctypes.byref(cache), accepted.data_ptr(), n_accepted.data_ptr(), N)
 
 
 def gpt_attn_pages_workspace_bytes(S, M, P) -> int:
+    if not _fits(S, M, P):
+        return 0
     return int(lib().gpt_attn_pages_workspace_bytes(int(S), int(M), int(P)))
 
 
@@ -716,11 +742,19 @@ def _check_state(table, refs, lens=None):
         raise ValueError("table must be an int32 tensor [S, M] and refs one [P]")
     S, M = table.shape
     P, dev = refs.shape[0], table.get_device()
+    if max(S, M, P) > _INT_MAX:
+        raise ValueError("table and refs must have fewer than 2^31 entries in each dimension")
     _check_int32("table", table, (S, M), dev)
     _check_int32("refs", refs, (P,), dev)
     if lens is not None:
         _check_int32("lens", lens, (S,), dev)
     return S, M, P, dev
+
+
+def _page_tokens(page):
+    if not -_INT_MAX <= page <= _INT_MAX:
+        raise ValueError("page must be less than 2^31")
+    return int(page)
 
 
 def _pages_workspace(workspace, S, M, P, table):
@@ -749,8 +783,8 @@ def gpt_attn_pages_reserve(table, lens, refs, page, tokens, status=None, workspa
     with _memory_of(stream, dev):
         status = _int32_out("status", status, (S,), tokens)
         ws = _pages_workspace(workspace, S, M, P, table)
-    _launch("gpt_attn_pages_reserve", dev, stream, table.data_ptr(), lens.data_ptr(), refs.data_ptr(), S, M, P, int(page),
-            tokens.data_ptr(), status.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
+    _launch("gpt_attn_pages_reserve", dev, stream, table.data_ptr(), lens.data_ptr(), refs.data_ptr(), S, M, P,
+            _page_tokens(page), tokens.data_ptr(), status.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
     _hand_over(stream, status)
     return status
 
@@ -766,8 +800,8 @@ def gpt_attn_pages_fork(table, lens, refs, page, parents, status=None, pairs=Non
         status = _int32_out("status", status, (S,), parents)
         pairs = _int32_out("pairs", pairs, (S, 2), table)
         ws = _pages_workspace(workspace, S, M, P, table)
-    _launch("gpt_attn_pages_fork", dev, stream, table.data_ptr(), lens.data_ptr(), refs.data_ptr(), S, M, P, int(page),
-            parents.data_ptr(), status.data_ptr(), pairs.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
+    _launch("gpt_attn_pages_fork", dev, stream, table.data_ptr(), lens.data_ptr(), refs.data_ptr(), S, M, P,
+            _page_tokens(page), parents.data_ptr(), status.data_ptr(), pairs.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
     _hand_over(stream, status, pairs)
     return status, pairs
 
@@ -802,6 +836,8 @@ def gpt_attn_pages_copy(k_pages, v_pages, pairs, n_pairs=None, stream=None):
     if pairs.dim() != 2:
         raise ValueError("pairs must be a contiguous int32 tensor [n, 2]")
     n = pairs.shape[0]
+    if n > _INT_MAX:
+        raise ValueError("pairs must have fewer than 2^31 rows")
     _check_int32("pairs", pairs, (n, 2), dev)
     if n_pairs is not None:
         _check_int32("n_pairs", n_pairs, (1,), dev)
