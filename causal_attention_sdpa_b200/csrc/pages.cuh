@@ -274,7 +274,8 @@ __device__ __forceinline__ int reserve_need(const PagesParams& p, int s) {
 }
 
 // Fork and reserve: every slot's wish, the free pages in order, then each slot's share of them.  A
-// slot is served if the wishes up to and including its own fit into the free pages.
+// slot is served if it asks for no page, or if the wishes up to and including its own fit into the free
+// pages.
 template <bool kFork>
 __global__ void __cluster_dims__(kPagesCluster, 1, 1) __launch_bounds__(kPagesThreads)
 pages_take_kernel(const __grid_constant__ PagesParams p) {
@@ -319,7 +320,7 @@ pages_take_kernel(const __grid_constant__ PagesParams p) {
         first = base + __shfl_sync(0xffffffffu, first, 0);
         base += n;
         if (s >= s_hi) continue;
-        const bool served = need >= 0 && (long long)first + need <= total_free;
+        const bool served = need == 0 || (need > 0 && (long long)first + need <= total_free);
         if (lane == 0) p.status[s] = need == -2 ? 0 : (served ? 1 : (need < 0 ? -1 : -2));
         int* row = p.table + (size_t)s * p.M;
         if (kFork) {

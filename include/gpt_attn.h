@@ -376,14 +376,15 @@ int gpt_attn_paged_accept(const gpt_attn_paged_cache* cache, const int* accepted
  * gpt_attn_pages_reserve: pages for tokens[s] more tokens than lens[s] (<= 0:
  *   nothing asked), behind those that the slot has.  -1 where M pages do not
  *   hold them.  A slot is served if what it and all slots before it ask for
- *   fits into the free pages.
+ *   fits into the free pages, or if its pages hold the tokens already.
  * gpt_attn_pages_fork: slot s becomes a copy of slot parents[s] (negative:
  *   nothing asked).  Full pages are shared (their refs go up); a partial last
  *   page gets a page of its own, the copy of which the caller makes with
  *   gpt_attn_pages_copy: pairs int32 [S, 2] receives (old, new), or (-1, -1).
  *   Pages that the parent holds past its last token are not shared.  -1 where s
  *   holds pages or tokens, the parent is not another slot that stays, or one of
- *   the parent's pages is missing.  Service is in order as above.
+ *   the parent's pages is missing.  Service is in order as above; a parent
+ *   whose last page is full asks for no page.
  * gpt_attn_pages_free: slots with drop[s] > 0 give their pages back (refs go
  *   down, the row is filled with -1, the length becomes 0).
  * gpt_attn_pages_compact: the new table, new refs and moves that pack the n

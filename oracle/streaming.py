@@ -104,7 +104,8 @@ def paged_decode(q, k_pages, v_pages, table, lens, parents=None, n_new=None, sca
 
 
 def _take(need, refs):
-    """Serves the slots' wishes in order (None: nothing asked, -1: refused): status and pages of each."""
+    """Serves the slots' wishes in order (None: nothing asked, -1: refused): status and pages of each.  A slot
+    that asks for no page needs none to be left."""
     free = [p for p, r in enumerate(refs) if r <= 0]
     status, got, base = [], [], 0
     for n in need:
@@ -112,7 +113,7 @@ def _take(need, refs):
             status.append(0 if n is None else -1)
             got.append([])
             continue
-        ok = base + n <= len(free)
+        ok = n == 0 or base + n <= len(free)
         status.append(1 if ok else -2)
         got.append(free[base:base + n] if ok else [])
         base += n
