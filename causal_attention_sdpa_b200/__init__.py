@@ -777,7 +777,7 @@ def _int32_out(name, t, shape, like):
 def gpt_attn_pages_reserve(table, lens, refs, page, tokens, status=None, workspace=None, stream=None):
     """Gives every slot pages for tokens[s] (int32 [S]) more tokens, the lowest free ones first; table
     and refs change in place.  Returns status int32 [S]: 0 nothing asked, 1 done, -1 refused (the table's
-    row is too short), -2 not enough free pages."""
+    row is too short, or has a page behind a -1), -2 not enough free pages."""
     S, M, P, dev = _check_state(table, refs, lens)
     _check_int32("tokens", tokens, (S,), dev)
     with _memory_of(stream, dev):

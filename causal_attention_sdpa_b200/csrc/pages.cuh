@@ -263,12 +263,21 @@ __device__ __forceinline__ int slot_pages(const PagesParams& p, int s) {
     return p.M;
 }
 
-// Reserve: pages for arg[s] more tokens than lens[s].
+// Whether slot s holds a page behind the first -1 of its row, that is past its `held` ones.
+__device__ __forceinline__ bool slot_gap(const PagesParams& p, int s, int held) {
+    bool page = false;
+    for (int j = held + (threadIdx.x & 31); j < p.M; j += 32) page |= p.table[(size_t)s * p.M + j] >= 0;
+    return __any_sync(0xffffffffu, page);
+}
+
+// Reserve: pages for arg[s] more tokens than lens[s].  They would overwrite the pages behind a gap, which
+// nobody could give back then.
 __device__ __forceinline__ int reserve_need(const PagesParams& p, int s) {
     const int more = p.arg[s], n = p.lens[s];
     if (more <= 0) return -2;
     if (n < 0 || (long long)n + more > (long long)p.M * p.page) return -1;
     const int held = slot_pages(p, s);
+    if (slot_gap(p, s, held)) return -1;
     const int want = (int)(((long long)n + more + p.page - 1) / p.page);
     return want > held ? want - held : 0;
 }

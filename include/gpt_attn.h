@@ -375,7 +375,9 @@ int gpt_attn_paged_accept(const gpt_attn_paged_cache* cache, const int* accepted
  *
  * gpt_attn_pages_reserve: pages for tokens[s] more tokens than lens[s] (<= 0:
  *   nothing asked), behind those that the slot has.  -1 where M pages do not
- *   hold them.  A slot is served if what it and all slots before it ask for
+ *   hold them, or where the row has a page behind an entry of -1 (entries that
+ *   a window has left behind may be cleared for gpt_attn_paged_decode, not for
+ *   these calls).  A slot is served if what it and all slots before it ask for
  *   fits into the free pages, or if its pages hold the tokens already.
  * gpt_attn_pages_fork: slot s becomes a copy of slot parents[s] (negative:
  *   nothing asked).  Full pages are shared (their refs go up); a partial last

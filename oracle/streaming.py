@@ -128,7 +128,8 @@ def pages_reserve(table, lens, refs, page, tokens):
     need = []
     for s, t in enumerate(tokens):
         n = int(lens[s]) + int(t)
-        need.append(None if t <= 0 else -1 if lens[s] < 0 or n > M * page else max(0, -(-n // page) - held[s]))
+        bad = lens[s] < 0 or n > M * page or (table[s, held[s]:] >= 0).any()
+        need.append(None if t <= 0 else -1 if bad else max(0, -(-n // page) - held[s]))
     status, got = _take(need, refs)
     for s, pages in enumerate(got):
         table[s, held[s]:held[s] + len(pages)] = pages
