@@ -709,8 +709,11 @@ int paged_strides(Strides* out, const gpt_attn_strides* in, const int* heads, in
     return GPT_ATTN_OK;
 }
 
+// The table kernels go through slots and pages in steps of up to 8192, so that a place past the last one has
+// to fit an int too.
 int check_pages(int S, int M, int P) {
-    if (S < 1 || M < 1 || P < 1) return GPT_ATTN_ERR_SHAPE;
+    constexpr int kMost = 0x7fffffff - 2 * kPagesCluster * kPagesThreads;
+    if (S < 1 || M < 1 || P < 1 || S > kMost || P > kMost) return GPT_ATTN_ERR_SHAPE;
     return (long long)S * M > 0x7fffffffLL ? GPT_ATTN_ERR_SHAPE : GPT_ATTN_OK;
 }
 

@@ -368,7 +368,8 @@ int gpt_attn_paged_accept(const gpt_attn_paged_cache* cache, const int* accepted
  * free).  Results do not depend on the order of threads: the lowest free pages
  * go to the lowest slots.  status int32 [S] is written for every slot: 0
  * nothing asked, 1 done, -1 refused, -2 not enough free pages; a slot with a
- * negative status is left as it was.  S, M, P >= 1 and S * M < 2^31.
+ * negative status is left as it was.  S, M, P >= 1, S * M < 2^31, and S and P
+ * no more than 2^31 - 2^15.
  * Asynchronous on `stream`; the workspace of reserve, fork and compact has
  * gpt_attn_pages_workspace_bytes(S, M, P) bytes, 16-byte aligned, contents
  * ignored on entry; calls that overlap on the GPU need one each.
