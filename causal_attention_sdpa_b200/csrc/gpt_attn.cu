@@ -1254,7 +1254,7 @@ void gpt_attn_tmap_cache_stats(long long* hits, long long* misses, int* entries)
 
 int gpt_attn_debug_skip_load(int which) {
 #ifdef GPT_ATTN_DEBUG
-    if (which < 0 || which > 2) return GPT_ATTN_ERR_SHAPE;
+    if (which < 0 || which > 3) return GPT_ATTN_ERR_SHAPE;
     return cudaMemcpyToSymbol(gpt_attn::g_debug_skip, &which, sizeof(int)) == cudaSuccess ? GPT_ATTN_OK
                                                                                          : GPT_ATTN_ERR_CUDA;
 #else

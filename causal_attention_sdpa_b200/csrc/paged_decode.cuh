@@ -392,6 +392,7 @@ __device__ __forceinline__ void paged_produce(const PagedParams& p, const CUtens
                 if (w * 32 < boxes) look_up(w);
         }
         if (i >= kStages && !warp_wait(&bar_empty[s], lap ^ 1, ac)) break;
+        if (which == 0 && debug_skip_load(3, i)) continue;   // debug builds: exercise the abort path
         if (lane == 0) {
             if (which == 0) {
                 tiles[i % kRing] = d;

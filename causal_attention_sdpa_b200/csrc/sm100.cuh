@@ -31,7 +31,7 @@ __device__ __forceinline__ bool debug_ok(bool cond) {
 #endif
 
 // True in a debug build when the producer of CTA 0 should skip the load of kind `which` (1 forward
-// K/V, 2 backward Q/dO) for its first tile.
+// K/V, 2 backward Q/dO, 3 paged decode's keys) for its first tile.
 __device__ __forceinline__ bool debug_skip_load(int which, int tile) {
 #ifdef GPT_ATTN_DEBUG
     return blockIdx.x == 0 && tile == 0 && *(volatile int*)&g_debug_skip == which;

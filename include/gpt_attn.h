@@ -472,6 +472,8 @@ void gpt_attn_tmap_cache_stats(long long* hits, long long* misses, int* entries)
  * kernels' own bounded waits run out and their abort path is exercised:
  *   which = 1 : the forward producer of CTA 0 skips its first K/V tile;
  *   which = 2 : the backward producer of CTA 0 skips its first Q/dO tile;
+ *   which = 3 : the key producers of CTA 0 of a paged decode skip their first
+ *               tile;
  *   which = 0 : no skip (normal operation).
  * A skipped load is neither issued nor announced to its barrier, so nothing
  * is left in flight: the consumer's wait runs out after the wait limit
