@@ -207,40 +207,32 @@ __device__ __forceinline__ bool paged_clean(uint8_t* v, const PagedTile& t, int 
     return odd;
 }
 
-// One warp works out the tree of sequence b: each node takes over the ancestors of the node it points at
-// and points where that one does, so 6 rounds reach 64 nodes up.
+// One warp works out the tree of sequence b, two nodes a lane: tree_step for all nodes at once, 6 times for 64.
 __device__ __forceinline__ void paged_tree(const PagedParams& p, int b, unsigned long long* anc, int* depth) {
     const int lane = threadIdx.x & 31;
-    unsigned long long a[2];
-    int up[2];
+    TreeNode x[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-        const int n = lane + 32 * e, to = n < p.N ? __ldg(p.parents + (size_t)b * p.N + n) : -1;
-        a[e] = 1ull << n;
-        up[e] = to < n ? to : -1;
+        const int n = lane + 32 * e;
+        x[e] = tree_node(n, n < p.N ? __ldg(p.parents + (size_t)b * p.N + n) : -1);
     }
 #pragma unroll 1
     for (int step = 1; step < p.N; step *= 2) {
-        unsigned long long more[2];
-        int next[2];
+        TreeNode next[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const int from = max(up[e], 0);
-            const unsigned long long a0 = __shfl_sync(0xffffffffu, a[0], from & 31), a1 = __shfl_sync(0xffffffffu, a[1], from & 31);
-            const int u0 = __shfl_sync(0xffffffffu, up[0], from & 31), u1 = __shfl_sync(0xffffffffu, up[1], from & 31);
-            more[e] = up[e] < 0 ? 0 : (from < 32 ? a0 : a1);
-            next[e] = up[e] < 0 ? -1 : (from < 32 ? u0 : u1);
+            const int from = max(x[e].up, 0);
+            const unsigned long long a0 = __shfl_sync(0xffffffffu, x[0].anc, from & 31), a1 = __shfl_sync(0xffffffffu, x[1].anc, from & 31);
+            const int u0 = __shfl_sync(0xffffffffu, x[0].up, from & 31), u1 = __shfl_sync(0xffffffffu, x[1].up, from & 31);
+            next[e] = tree_step(x[e], TreeNode{from < 32 ? a0 : a1, from < 32 ? u0 : u1});
         }
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            a[e] |= more[e];
-            up[e] = next[e];
-        }
+        for (int e = 0; e < 2; ++e) x[e] = next[e];
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-        anc[lane + 32 * e] = a[e];
-        depth[lane + 32 * e] = __popcll(a[e]) - 1;
+        anc[lane + 32 * e] = x[e].anc;
+        depth[lane + 32 * e] = __popcll(x[e].anc) - 1;
     }
 }
 
@@ -351,8 +343,7 @@ __device__ __forceinline__ void paged_produce(const PagedParams& p, const CUtens
         int row[kWords];
 #pragma unroll
         for (int w = 0; w < kWords; ++w)
-            if (w * 32 < boxes)
-                row[w] = entry[w] < 0 || entry[w] >= p.n_pages ? -1 : (entry[w] * p.Hkv + h) * p.page.d + in_page[w];
+            if (w * 32 < boxes) row[w] = pool_row(entry[w], in_page[w], p.page, p.n_pages, p.Hkv, h);
         PagedTile d;
         if (which == 0) {
             d.key0 = sp.tile(at.t) * kTile;

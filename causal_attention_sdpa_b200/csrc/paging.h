@@ -1,7 +1,7 @@
 // Index arithmetic of the paged cache, as plain integer code: which key tiles a sequence's new
 // tokens visit, which keys a node of a draft tree sees, and where a position lives.  nvcc compiles
-// it into the kernels; the CPU tests compile the same header with a host compiler and check it
-// against brute force.
+// it into the kernels (paged_ancestors aside, which the tests go by); the CPU tests compile the same
+// header with a host compiler and check it against brute force.
 #pragma once
 
 #include "schedule.h"
@@ -65,8 +65,20 @@ GPT_ATTN_HD PagedSpan paged_span(int len, int n_new, int cap, int window, int si
     return s;
 }
 
-// Ancestors (itself included) of node i, by its parents; a parent that is not before its child
-// counts as the cached context.
+// A node on its way to its ancestors: those known so far (itself included), and the next one up, -1: none.
+struct TreeNode {
+    unsigned long long anc;
+    int up;
+};
+// Node n before the first step; a parent that is not before its child counts as the cached context.
+GPT_ATTN_HD TreeNode tree_node(int n, int parent) { return TreeNode{1ull << n, parent < n ? parent : -1}; }
+// One step of all nodes at once doubles how far each has come: it takes over the ancestors of the node that it
+// points at, and points where that one did.
+GPT_ATTN_HD TreeNode tree_step(TreeNode x, TreeNode up) {
+    return TreeNode{x.anc | (x.up < 0 ? 0 : up.anc), x.up < 0 ? -1 : up.up};
+}
+
+// Ancestors (itself included) of node i, parent by parent: what the steps above have to come to.
 GPT_ATTN_HD unsigned long long paged_ancestors(int i, const int* parents) {
     unsigned long long m = 1ull << i;
     while (parents[i] >= 0 && parents[i] < i) {
@@ -102,11 +114,16 @@ GPT_ATTN_HD unsigned paged_sees(int key0, int L, int lower, int sinks, unsigned 
     return cached | (unsigned)(at >= 0 ? vis << at : vis >> -at);
 }
 
-// Row of position `key` of a sequence within a pool [n_pages, Hkv, page, D], in rows of D; -1 if
-// its page is missing.
+// Row `in_page` of head h of page `entry` of a pool [n_pages, Hkv, page, D], in rows of D; -1 if there is no
+// such page.
+GPT_ATTN_HD int pool_row(int entry, int in_page, const FastDiv& page, int n_pages, int Hkv, int h) {
+    return entry < 0 || entry >= n_pages ? -1 : (entry * Hkv + h) * page.d + in_page;
+}
+
+// Row of position `key` of a sequence.
 GPT_ATTN_HD int paged_row(const int* table_row, int key, const FastDiv& page, int n_pages, int Hkv, int h) {
-    const int j = page.div(key), e = table_row[j];
-    return e < 0 || e >= n_pages ? -1 : (e * Hkv + h) * page.d + (key - j * page.d);
+    const int j = page.div(key);
+    return pool_row(table_row[j], key - j * page.d, page, n_pages, Hkv, h);
 }
 
 // Rows of a page that one load brings: the largest power of two that divides the page, up to
@@ -116,10 +133,10 @@ GPT_ATTN_HD int paged_box(int page) {
     return box < kPagedBox ? box : kPagedBox;
 }
 
-// The flattened list of tiles of all items is cut into pieces of `chunk` tiles, one to a block;
-// at least `least` to a piece, so that short calls are not scattered.
-GPT_ATTN_HD int paged_chunk(int total, int blocks, int least) {
-    const int c = total / blocks + (total % blocks > 0);
+// The list of all items' tiles and costs is cut into pieces of `chunk`, one to each of `workers` (teams of
+// warps), none shorter than `least`.
+GPT_ATTN_HD int paged_chunk(int total, int workers, int least) {
+    const int c = total / workers + (total % workers > 0);
     return c < least ? least : c;
 }
 
