@@ -28,8 +28,15 @@
 // Measured on one B200: one token of 16 sequences of 16384 (6 heads of 128) 134 us, 6.0 TB/s; of 64
 // sequences of 4096 (12 heads of 64, pages of 16) 136 us, 5.9 TB/s; of 64 up to 1024 32 us, 3.9 TB/s; of
 // one of 777 9 us.  Some 11 us of a call are launches, the first loads and the join.
-// Statistics and accumulators are fp32; P is rounded to bf16 for the second product, as in the
-// forward kernel, while its sum is taken before the rounding.
+// Statistics and accumulators are fp32.  The second product takes bf16 inputs.  With up to 16 rows P goes into
+// it as two terms, its rounding and what that left out, so that O is as exact as attn_decode.cuh's, which keeps
+// P in fp32: an error of O's own rounding alone, 0.0016 of its norm, where one term has 0.0020.  Loads bound
+// those calls, and the second term costs one token of 64 sequences of up to 1024 3 % (48.4 against 46.8 us,
+// caches cold), 4 to 16 rows over 16 sequences of 4096 1 to 2 %, one token over longer contexts nothing that shows
+// (118.5 against 120.8 us, 120.8 against 120.0).  With more rows it would cost
+// 8 to 11 % (8 rows of 4 heads over 8192: 44.5 against 40.9 us; 13 of 4 under a window of 4096 on the tcgen05
+// tiles: 75 against 67), and P is rounded once, as in the forward kernel of the training calls; its sum is
+// taken before the rounding.
 #pragma once
 
 #include "attn_fwd.cuh"
@@ -109,6 +116,11 @@ __device__ __forceinline__ bool not_finite(uint32_t w) {
 // Two packed bf16 values with 0 in place of infinities and NaN.
 __device__ __forceinline__ uint32_t finite_bf16x2(uint32_t w) {
     return ((w & 0x7f80u) == 0x7f80u ? 0u : w & 0xffffu) | ((w & 0x7f800000u) == 0x7f800000u ? 0u : w & 0xffff0000u);
+}
+
+// What rounding lo and hi to the two bf16 values in `w` left out, rounded itself: together they hold 16 bits.
+__device__ __forceinline__ uint32_t rest_bf16x2(float lo, float hi, uint32_t w) {
+    return pack_bf16x2(lo - __uint_as_float(w << 16), hi - __uint_as_float(w & 0xffff0000u));
 }
 
 template <int D>
@@ -418,6 +430,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     constexpr int NT = kKeys / 8;
     constexpr int kChunks = D / 8;                   // 16-byte chunks of a row
     constexpr int kRows = 16 * MT;
+    constexpr bool kTwoTerms = MT == 1;              // P in two bf16 terms
     extern __shared__ uint8_t smem_raw[];
     PagedSmem<D>& block = *reinterpret_cast<PagedSmem<D>*>(smem_align1024(smem_raw));
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -635,7 +648,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             }
         }
         const float mu0 = m[0] == -INFINITY ? 0.f : m[0], mu1 = m[1] == -INFINITY ? 0.f : m[1];
-        uint32_t pf[NT / 2][4];
+        uint32_t pf[NT / 2][4], pl[kTwoTerms ? NT / 2 : 1][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const float p0 = ex2_approx(fmaf(sc[n][0], p.scale_log2, -mu0)), p1 = ex2_approx(fmaf(sc[n][1], p.scale_log2, -mu0));
@@ -644,6 +657,10 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             l[1] += p2 + p3;
             pf[n / 2][(n & 1) * 2] = pack_bf16x2(p0, p1);
             pf[n / 2][(n & 1) * 2 + 1] = pack_bf16x2(p2, p3);
+            if constexpr (kTwoTerms) {
+                pl[n / 2][(n & 1) * 2] = rest_bf16x2(p0, p1, pf[n / 2][(n & 1) * 2]);
+                pl[n / 2][(n & 1) * 2 + 1] = rest_bf16x2(p2, p3, pf[n / 2][(n & 1) * 2 + 1]);
+            }
         }
         // Rows that came along in a box without being seen may hold anything, and new tokens that are not
         // every node's ancestors infinities and NaN, which must not reach the others through 0 * NaN.
@@ -729,6 +746,10 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                     ldmatrix4_trans(b4, v_addr + paged_at<kTile>(key, n * 2 + (lane >> 4)) + kk * 16 * 128);
                     mma_16816(oacc[2 * n], pf[kk], b4[0], b4[1]);
                     mma_16816(oacc[2 * n + 1], pf[kk], b4[2], b4[3]);
+                    if constexpr (kTwoTerms) {
+                        mma_16816(oacc[2 * n], pl[kk], b4[0], b4[1]);
+                        mma_16816(oacc[2 * n + 1], pl[kk], b4[2], b4[3]);
+                    }
                 }
             }
         }
