@@ -200,18 +200,20 @@ bool launch_dependent(void (*kernel)(Params...), dim3 grid, unsigned threads, si
 int sm_count();
 
 // Kernel-side mask parameters from the C ABI's description (nullptr: plain causal).  Per-head
-// windows are copied out of the caller's host array into the kernel parameters.
-int make_mask(MaskParams* m, const gpt_attn_mask* a, int H) {
+// windows are copied out of the caller's host array into the kernel parameters.  A window past T acts as one of
+// T, so that sums of positions and windows fit an int.
+int make_mask(MaskParams* m, const gpt_attn_mask* a, int H, int T) {
     memset(m, 0, sizeof(*m));
     m->H = H;
     if (!a) return GPT_ATTN_OK;
-    m->window = a->window > 0 ? a->window : 0;
+    auto within = [&](int w) { return w <= 0 ? 0 : (w < T ? w : T); };
+    m->window = within(a->window);
     m->doc_start = a->doc_start;
     if (a->doc_start && (reinterpret_cast<uintptr_t>(a->doc_start) & 3u)) return GPT_ATTN_ERR_ALIGN;
     if (a->head_windows) {
         if (H > kMaxHeadWindows) return GPT_ATTN_ERR_SHAPE;
         m->head_windows = 1;
-        for (int h = 0; h < H; ++h) m->win[h] = a->head_windows[h] > 0 ? a->head_windows[h] : 0;
+        for (int h = 0; h < H; ++h) m->win[h] = within(a->head_windows[h]);
     }
     return GPT_ATTN_OK;
 }
@@ -231,10 +233,10 @@ bool sink_mask(SinkMask* s, const MaskParams& m, int sinks, int H, int T) {
     return sinks > 0 && any;
 }
 
-MaskParams window_mask(int window, int H) {
+MaskParams window_mask(int window, int H, int T) {
     gpt_attn_mask a{window, nullptr, nullptr};
     MaskParams m;
-    make_mask(&m, &a, H);
+    make_mask(&m, &a, H, T);
     return m;
 }
 
@@ -783,7 +785,7 @@ int gpt_attn_fwd_sinks(const void* q, const void* k, const void* v, void* o, flo
     if (sc != GPT_ATTN_OK) return sc;
     if (misaligned(q) || misaligned(k) || misaligned(v) || misaligned(o) || misaligned(lse)) return GPT_ATTN_ERR_ALIGN;
     MaskParams m;
-    if ((sc = make_mask(&m, mask, H)) != GPT_ATTN_OK) return sc;
+    if ((sc = make_mask(&m, mask, H, T)) != GPT_ATTN_OK) return sc;
     Layout L;
     if ((sc = make_layout(&L, layout, H, T, D)) != GPT_ATTN_OK) return sc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -818,7 +820,7 @@ int gpt_attn_bwd_delta(const void* o, const float* lse, const void* dO, int B, i
     if (sc != GPT_ATTN_OK) return sc;
     if ((sc = check_ws(B, H, T, D, workspace, workspace_bytes)) != GPT_ATTN_OK) return sc;
     if (misaligned(o) || misaligned(lse) || misaligned(dO)) return GPT_ATTN_ERR_ALIGN;
-    return launch_bwd_delta(o, lse, dO, B, H, T, D, workspace, window_mask(0, H), contiguous_layout(H, T, D),
+    return launch_bwd_delta(o, lse, dO, B, H, T, D, workspace, window_mask(0, H, T), contiguous_layout(H, T, D),
                             static_cast<cudaStream_t>(stream));
 }
 
@@ -832,7 +834,7 @@ int gpt_attn_bwd_grads(const void* q, const void* k, const void* v, const void* 
     if (misaligned(q) || misaligned(k) || misaligned(v) || misaligned(dO) || misaligned(dk) || misaligned(dv))
         return GPT_ATTN_ERR_ALIGN;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const MaskParams m = window_mask(window, H);
+    const MaskParams m = window_mask(window, H, T);
     const Layout L = contiguous_layout(H, T, D);
     return D == 64 ? launch_bwd_grads<64>(q, k, v, dO, dk, dv, B, H, T, scale, m, L, workspace, st)
                    : launch_bwd_grads<128>(q, k, v, dO, dk, dv, B, H, T, scale, m, L, workspace, st);
@@ -866,7 +868,7 @@ int gpt_attn_bwd_sinks(const void* q, const void* k, const void* v, const void* 
         misaligned(dq) || misaligned(dk) || misaligned(dv))
         return GPT_ATTN_ERR_ALIGN;
     MaskParams m;
-    if ((sc = make_mask(&m, mask, H)) != GPT_ATTN_OK) return sc;
+    if ((sc = make_mask(&m, mask, H, T)) != GPT_ATTN_OK) return sc;
     Layout L;
     if ((sc = make_layout(&L, layout, H, T, D)) != GPT_ATTN_OK) return sc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -77,3 +77,24 @@ def test_page_sizes_past_an_int_are_refused():
             ga.gpt_attn_pages_reserve(z(2, 3) - 1, z(2), z(9), page, z(2))
         with pytest.raises(ValueError):
             ga.gpt_attn_pages_fork(z(2, 3) - 1, z(2), z(9), page, z(2) - 1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("x", [500, 501, 2 ** 30, TOP - 1, TOP, 2 ** 31, 2 ** 40])
+def test_backward_with_windows_past_the_row(x, D):
+    """Positions and such windows add up past an int, so they are cut to the row's length first."""
+    gpu()
+    q, k, v, do = (t.cuda() for t in make_inputs(2, 2, 500, D, seed=1))
+    o, lse = ga.gpt_attn_fwd(q, k, v, window=x)
+    o2, lse2 = ga.gpt_attn_fwd(q, k, v)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    g, g2 = ga.gpt_attn_bwd(q, k, v, o, lse, do, window=x), ga.gpt_attn_bwd(q, k, v, o, lse, do)
+    assert torch.equal(g[1], g2[1]) and torch.equal(g[2], g2[2])
+    kw, low = dict(head_windows=[x, 60], doc_start=None), dict(head_windows=[0, 60], doc_start=None)
+    for _ in range(2):
+        o, lse = ga.gpt_attn_fwd_ex(q, k, v, **kw)
+        assert torch.equal(o, ga.gpt_attn_fwd_ex(q, k, v, **low)[0])
+        g, g2 = ga.gpt_attn_bwd_ex(q, k, v, o, lse, do, **kw), ga.gpt_attn_bwd_ex(q, k, v, o, lse, do, **low)
+        assert torch.equal(g[1], g2[1]) and torch.equal(g[2], g2[2])
+        kw["doc_start"] = low["doc_start"] = torch.tensor([[0] * 130 + [130] * 370] * 2, dtype=torch.int32, device="cuda")
