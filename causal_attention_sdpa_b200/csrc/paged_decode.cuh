@@ -25,18 +25,21 @@
 // A warp's steps on a tile depend on one another, so their latency counts, not their number: two teams
 // share one block because its warps can then have 208 registers each (blocks of one team put five warps
 // on an SM sub-partition's registers and spilled).
-// Measured on one B200: one token of 16 sequences of 16384 (6 heads of 128) 134 us, 6.0 TB/s; of 64
-// sequences of 4096 (12 heads of 64, pages of 16) 136 us, 5.9 TB/s; of 64 up to 1024 32 us, 3.9 TB/s; of
-// one of 777 9 us.  Some 11 us of a call are launches, the first loads and the join.
-// Statistics and accumulators are fp32.  The second product takes bf16 inputs.  With up to 16 rows P goes into
-// it as two terms, its rounding and what that left out, so that O is as exact as attn_decode.cuh's, which keeps
-// P in fp32: an error of O's own rounding alone, 0.0016 of its norm, where one term has 0.0020.  Loads bound
-// those calls, and the second term costs one token of 64 sequences of up to 1024 3 % (48.4 against 46.8 us,
-// caches cold), 4 to 16 rows over 16 sequences of 4096 1 to 2 %, one token over longer contexts nothing that shows
-// (118.5 against 120.8 us, 120.8 against 120.0).  With more rows it would cost
-// 8 to 11 % (8 rows of 4 heads over 8192: 44.5 against 40.9 us; 13 of 4 under a window of 4096 on the tcgen05
-// tiles: 75 against 67), and P is rounded once, as in the forward kernel of the training calls; its sum is
-// taken before the rounding.
+// Measured on one B200: one token of 16 sequences of 16384 (6 heads of 128) 132 us, 6.1 TB/s; of 64
+// sequences of 4096 (12 heads of 64, pages of 16) 133 us, 6.1 TB/s; of 64 up to 1024 32 us, 3.9 TB/s; of
+// one of 777 9 us.  Calls on many sequences take some 9 to 13 us more than their bytes at a copy's rate:
+// launches, the first loads and the joins.
+// Statistics and accumulators are fp32.  The second product takes bf16 inputs.  With up to 16 rows P goes
+// into it as two terms, its rounding and what that left out, so that O is as exact as attn_decode.cuh's,
+// which keeps P in fp32: an error of O's own rounding alone, 0.0016 of its norm, where one term has 0.0020.
+// With up to 8 rows the second terms are the rows of the 16-row tile that the item does not have, and their
+// sums are added at its end: no product more, and no exponentials for rows that are not there (one token of
+// 64 sequences of up to 1024 31.8 us, where P rounded once and 16 rows' work took 33.2; of 16 of 16384 the
+// same).  With products of their own, which 9 to 16 rows have, the second terms cost those calls 7 %; 16
+// rows over 16 sequences of 4096 take 40.5 us where one term took 40.0.  More rows would pay 8 to 11 % (8
+// rows of 4 heads over 8192: 44.5 against 40.9 us; 13 of 4 under a window of 4096 on the tcgen05 tiles: 75
+// against 67), and P is rounded once, as in the forward kernel of the training calls.  P's sum is taken
+// before the rounding.
 #pragma once
 
 #include "attn_fwd.cuh"
@@ -419,7 +422,9 @@ __device__ __forceinline__ void paged_produce(const PagedParams& p, const CUtens
     for (int j = max(0, i - kStages); j < i; ++j) mbar_wait_drain(&bar_full[j % kStages], (j / kStages) & 1, p.timeout_ns);
 }
 
-template <int D, int MT>
+// MT: 16-row tiles of an item's rows.  kFold: the item has up to 8 rows, whose second terms of P take the
+// place of the tile's other 8.
+template <int D, int MT, bool kFold>
 __global__ void __launch_bounds__(kPagedThreads, 1)
 paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const __grid_constant__ PagedParams p) {
@@ -430,7 +435,9 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     constexpr int NT = kKeys / 8;
     constexpr int kChunks = D / 8;                   // 16-byte chunks of a row
     constexpr int kRows = 16 * MT;
-    constexpr bool kTwoTerms = MT == 1;              // P in two bf16 terms
+    static_assert(!kFold || MT == 1, "one tile");
+    constexpr bool kTwoTerms = MT == 1 && !kFold;    // P in two bf16 terms, each in products of its own
+    constexpr int kE = kFold ? 1 : 2;                // rows of a thread: r_lo, r_lo + 8
     extern __shared__ uint8_t smem_raw[];
     PagedSmem<D>& block = *reinterpret_cast<PagedSmem<D>*>(smem_align1024(smem_raw));
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -493,7 +500,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     unsigned long long vis[2];                       // 0: no such row, or no such node
     int node[2], head[2];                            // node, and head within the group, of the two rows; -1: no row
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
+    for (int e = 0; e < kE; ++e) {
         const int r = r_lo + 8 * e, hd = p.by_n.div(r);
         head[e] = r < p.R ? hd : -1;
         node[e] = r - hd * p.N;
@@ -550,7 +557,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             }
         }
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int e = 0; e < kE; ++e) {
             const bool live = head[e] >= 0 && node[e] < sp.n;
             const int pos = sp.L + sm.depth[tree][node[e]];
             lower[e] = paged_lower(pos, p.window);
@@ -605,7 +612,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         if (partial) {
             const int key0 = t.key0 + kb;
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
+            for (int e = 0; e < kE; ++e)
 #pragma unroll
                 for (int w = 0; w < (NT + 3) / 4; ++w) {
                     // this lane's keys of the word: bits 0 and 1, 8 and 9, ...
@@ -625,20 +632,21 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             mx[0] = fmaxf(mx[0], fmaxf(sc[n][0], sc[n][1]));
-            mx[1] = fmaxf(mx[1], fmaxf(sc[n][2], sc[n][3]));
+            if constexpr (!kFold) mx[1] = fmaxf(mx[1], fmaxf(sc[n][2], sc[n][3]));
         }
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int e = 0; e < kE; ++e) {
             mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
             mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2)) * p.scale_log2;
         }
-        const bool grow0 = mx[0] > m[0] + kLazyRescale, grow1 = mx[1] > m[1] + kLazyRescale;
+        const bool grow0 = mx[0] > m[0] + kLazyRescale, grow1 = !kFold && mx[1] > m[1] + kLazyRescale;
         if (__any_sync(0xffffffffu, grow0 || grow1)) {
-            const float a0 = grow0 ? ex2_approx(m[0] - mx[0]) : 1.f, a1 = grow1 ? ex2_approx(m[1] - mx[1]) : 1.f;
+            const float a0 = grow0 ? ex2_approx(m[0] - mx[0]) : 1.f;
+            const float a1 = kFold ? a0 : (grow1 ? ex2_approx(m[1] - mx[1]) : 1.f);
             if (grow0) m[0] = mx[0];
             if (grow1) m[1] = mx[1];
             l[0] *= a0;
-            l[1] *= a1;
+            if constexpr (!kFold) l[1] *= a1;
 #pragma unroll
             for (int n = 0; n < D / 8; ++n) {
                 oacc[n][0] *= a0;
@@ -647,19 +655,26 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 oacc[n][3] *= a1;
             }
         }
-        const float mu0 = m[0] == -INFINITY ? 0.f : m[0], mu1 = m[1] == -INFINITY ? 0.f : m[1];
-        uint32_t pf[NT / 2][4], pl[kTwoTerms ? NT / 2 : 1][4];
+        const float mu0 = m[0] == -INFINITY ? 0.f : m[0], mu1 = kFold || m[1] == -INFINITY ? 0.f : m[1];
+        uint32_t pf[NT / 2][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const float p0 = ex2_approx(fmaf(sc[n][0], p.scale_log2, -mu0)), p1 = ex2_approx(fmaf(sc[n][1], p.scale_log2, -mu0));
-            const float p2 = ex2_approx(fmaf(sc[n][2], p.scale_log2, -mu1)), p3 = ex2_approx(fmaf(sc[n][3], p.scale_log2, -mu1));
+            uint32_t(&a)[4] = pf[n / 2];
+            const int x = (n & 1) * 2;
             l[0] += p0 + p1;
-            l[1] += p2 + p3;
-            pf[n / 2][(n & 1) * 2] = pack_bf16x2(p0, p1);
-            pf[n / 2][(n & 1) * 2 + 1] = pack_bf16x2(p2, p3);
-            if constexpr (kTwoTerms) {
-                pl[n / 2][(n & 1) * 2] = rest_bf16x2(p0, p1, pf[n / 2][(n & 1) * 2]);
-                pl[n / 2][(n & 1) * 2 + 1] = rest_bf16x2(p2, p3, pf[n / 2][(n & 1) * 2 + 1]);
+            a[x] = pack_bf16x2(p0, p1);
+            if constexpr (kFold) {
+                a[x + 1] = rest_bf16x2(p0, p1, a[x]);
+            } else {
+                const float p2 = ex2_approx(fmaf(sc[n][2], p.scale_log2, -mu1));
+                const float p3 = ex2_approx(fmaf(sc[n][3], p.scale_log2, -mu1));
+                l[1] += p2 + p3;
+                a[x + 1] = pack_bf16x2(p2, p3);
+                sc[n][0] = p0;
+                sc[n][1] = p1;
+                sc[n][2] = p2;
+                sc[n][3] = p3;
             }
         }
         // Rows that came along in a box without being seen may hold anything, and new tokens that are not
@@ -717,7 +732,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                         if (!not_finite(w)) continue;
                         const float x0 = __uint_as_float(w << 16), x1 = __uint_as_float(w & 0xffff0000u);
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
+                        for (int e = 0; e < kE; ++e) {
                             if (__bfloat162float(pw[(lane >> 2) + 8 * e][kk]) == 0.f) continue;
                             if (!isfinite(x0)) oacc[n][2 * e] += x0;
                             if (!isfinite(x1)) oacc[n][2 * e + 1] += x1;
@@ -740,6 +755,14 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             const int key = kb + (lane & 15);
 #pragma unroll
             for (int kk = 0; kk < NT / 2; ++kk) {
+                uint32_t rest[4];
+                if constexpr (kTwoTerms) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float* x = &sc[2 * kk + (e >> 1)][(e & 1) * 2];
+                        rest[e] = rest_bf16x2(x[0], x[1], pf[kk][e]);
+                    }
+                }
 #pragma unroll
                 for (int n = 0; n < D / 16; ++n) {
                     uint32_t b4[4];
@@ -747,8 +770,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                     mma_16816(oacc[2 * n], pf[kk], b4[0], b4[1]);
                     mma_16816(oacc[2 * n + 1], pf[kk], b4[2], b4[3]);
                     if constexpr (kTwoTerms) {
-                        mma_16816(oacc[2 * n], pl[kk], b4[0], b4[1]);
-                        mma_16816(oacc[2 * n + 1], pl[kk], b4[2], b4[3]);
+                        mma_16816(oacc[2 * n], rest, b4[0], b4[1]);
+                        mma_16816(oacc[2 * n + 1], rest, b4[2], b4[3]);
                     }
                 }
             }
@@ -759,8 +782,15 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             // ---- end of the item (or of this team's part)
             const int b = at.b, h = at.h;
             const bool whole = done && first == 0;
+            if constexpr (kFold) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+                for (int n = 0; n < D / 8; ++n) {
+                    oacc[n][0] += oacc[n][2];
+                    oacc[n][1] += oacc[n][3];
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < kE; ++e) {
                 l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
                 l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
                 if (vis[e] == 0) {                   // a row or node that does not exist sees nothing
@@ -776,7 +806,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             const int par = item++ & 1;
             if ((lane & 3) == 0) {
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
+                for (int e = 0; e < kE; ++e) {
                     sm.m[par][w4][(lane >> 2) + 8 * e] = m[e];
                     sm.l[par][w4][(lane >> 2) + 8 * e] = l[e];
                 }
@@ -784,7 +814,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             if (!join()) return;
             float2* state = reinterpret_cast<float2*>(sm.kv[s]);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+            for (int e = 0; e < kE; ++e) {
                 const int r = (lane >> 2) + 8 * e;
                 if (vis[e] == 0) continue;
 #pragma unroll

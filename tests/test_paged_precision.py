@@ -12,7 +12,8 @@ from test_paged import cuda, make_cache, random_trees
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("G,N,lens,W", [(1, 1, [3, 9, 30, 1, 70, 17], 0), (4, 1, [5, 12, 2, 40], 0), (16, 1, [7, 20], 0),
                                         (1, 16, [4, 11, 2], 0), (2, 8, [6, 25], 10), (1, 5, [300, 1000, 4], 9),
-                                        (3, 5, [129, 5], 0)])
+                                        (3, 5, [129, 5], 0), (8, 1, [700, 5, 33], 0), (9, 1, [700, 5, 33], 0),
+                                        (1, 8, [60, 2], 30), (1, 9, [60, 2], 30)])
 def test_one_rounding(G, N, lens, W, D):
     """P enters the second product in two bf16 terms.  Each is off by 2^-8 of what it rounds at most, so P
     is by 2^-16; scores are fp32 sums of up to 128 products, which with the exponential leaves P off by less
