@@ -26,8 +26,11 @@
 //                          fp32 accumulator by TMA bulk reduce-adds from a
 //                          dedicated warpgroup.
 //   attn_dq_convert_kernel dQ = bf16(scale * fp32 accumulator).
-// dS is rounded to bf16 unscaled; the score scale is applied once per output
-// element, in the dK epilogue and in the dQ conversion.
+// P and dS enter their products in bf16, the type of the other operand; Delta is
+// taken from O as it was rounded.  dV is off by 0.0023 of its norm, dQ and dK by
+// 0.0024, of which their own rounding is 0.0017 (T=512, D=64 and 128).  dS is
+// rounded unscaled; the score scale is applied once per output element, in the
+// dK epilogue and in the dQ conversion.
 // The kernel below serves D = 128, whose accumulators fill all 512 TMEM columns
 // (S^T, then P^T over it; dP^T, then dQ over it; dV; dK), so one query tile's
 // P/dS pass runs at a time.  Its five 8-step MMA chains go out from three
@@ -165,7 +168,8 @@ struct BwdSmem {
 // dO_i . O_i takes over the rounding of O to bf16, which weighs most where dS is small against P dP, that
 // is where a row sees few keys.  At T=37 with all keys in reach dQ and dK come from 0.00276 to 0.00241 of exact
 // (relative norm, of which 0.0024 are their own rounding and that of dS), at T=512, window 8, 4 sinks from
-// 0.00263 to 0.00235.  A warp to a row, D / 8 lanes to a key; of each head the first `rows` rows are looked at.
+// 0.00263 to 0.00235.  Rows of more keys keep the rounding, which fades with their number: dQ is off by 0.0025
+// with 18 keys in reach, 0.0025 with 32, 0.0024 with 64, where 16 give 0.0023.  A warp to a row, D / 8 lanes to a key; of each head the first `rows` rows are looked at.
 // In the prep kernel, whose registers it doubled, this cost 13 us of 115 at B=8 H=12 T=1024 D=64; in a kernel
 // of its own 3; launched so that it runs beside the prep kernel, which leaves these rows out, 2.
 constexpr int kExactDelta = 16;
@@ -236,6 +240,8 @@ __device__ __forceinline__ void exact_delta(const DeltaKeys& p, const SinkMask& 
     if (lane == 0) p.delta[(size_t)bh * p.T_pad + t] = sum;
 }
 
+// Runs beside the prep kernel, which is an ordinary launch and writes neither this kernel's inputs nor the rows
+// of Delta that this one writes (both go by sink_keys): only its end has to wait.
 template <int D>
 __global__ void __launch_bounds__(256) attn_exact_delta_kernel(const DeltaKeys p, const SinkMask mask) {
     const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);

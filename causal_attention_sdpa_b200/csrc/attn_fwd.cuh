@@ -40,6 +40,11 @@
 // probability then stays <= 2^8, and since the final O / l and lse use the same
 // reference max the result is unchanged.
 //
+// P enters the second product in bf16, the type of V; its sum is taken before the
+// rounding.  O is off by 0.0020 to 0.0022 of its norm, of which its own rounding is
+// 0.0016.  A second term of P (paged_decode.cuh) would be twice the products and
+// conversions of this pass.
+//
 // Key tiles entirely after a Q tile's last query, or entirely before the window
 // of its first query, are never loaded for it; only the diagonal tile and the
 // window-edge tiles evaluate the visibility predicate.

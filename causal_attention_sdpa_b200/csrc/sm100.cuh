@@ -61,8 +61,10 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
 
 // ---------------------------------------------------------------- dependent launches
 // A kernel launched with launch_dependent (gpt_attn.cu) may start once all blocks of the one before it
-// in the stream have called launch_dependents.  Before it touches anything, every thread of it waits
-// until that kernel has ended.
+// in the stream have called launch_dependents.  That one is an ordinary launch, so all before it has ended.
+// Every thread waits until that kernel has ended, before it reads what that kernel writes or writes what that
+// kernel reads or writes, and in any case before it ends itself: what comes next in the stream waits for the
+// end of this one only.
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_prerequisites() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
