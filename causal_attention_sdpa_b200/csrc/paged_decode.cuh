@@ -201,9 +201,9 @@ struct PagedSmem {
 };
 
 // A team's pass over the values of a tile some rows of which are not to be used: unseen rows are cleared
-// and, if `check`, infinities and NaN of the others looked for.  The pass
-// runs a few times a call, so that its instructions are waited for: not unrolled, the tcgen05 kernel
-// gains 2 us of 61; the other gains more from the schedule of its other loops beside the unrolled one.
+// and, if `check`, infinities and NaN of the others looked for.  The pass runs a few times a call, so that its
+// instructions are waited for: not unrolled, the tcgen05 kernel gains 2 us of 61.  The kernel for up to 32 rows
+// takes the same time either way (8 nodes over 16 sequences of 3000: 29.0 and 29.2 us).
 template <int D, int kTile, int kUnroll>
 __device__ __forceinline__ bool paged_clean(uint8_t* v, const PagedTile& t, int tid, bool check) {
     constexpr int kPerRow = kPagedTeam / kTile, kMine = D / 8 / kPerRow;      // threads to a row, 16-byte chunks of each
@@ -692,23 +692,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             __syncwarp();
         } else if (mask) {
             uint4* rows = reinterpret_cast<uint4*>(vt);
-            bool odd = false;
-            if constexpr (MT == 2) {
-                odd = paged_clean<D, kTile, D / 8>(vt, t, tid, sp.differs(t.key0, kTile, p.window));
-            } else {
-                // chunk by chunk: 134 against 155 us with the pass above for one token of 16 sequences of 16384
-                // (6 heads of 128), which does not even come here, by how the rest is scheduled beside it
-#pragma unroll 2
-                for (int c = tid; c < kTile * kChunks; c += kPagedTeam) {
-                    const int key = (c >> 3) & (kTile - 1);
-                    if (!((t.seen[key >> 5] >> (key & 31)) & 1)) {
-                        rows[c] = make_uint4(0u, 0u, 0u, 0u);
-                    } else if (p.N > 1) {
-                        const uint4 x = rows[c];
-                        odd = odd || not_finite(x.x) || not_finite(x.y) || not_finite(x.z) || not_finite(x.w);
-                    }
-                }
-            }
+            bool odd = paged_clean<D, kTile, D / 8>(vt, t, tid, sp.differs(t.key0, kTile, p.window));
             odd = __any_sync(0xffffffffu, odd);
             int(&any)[kPagedTeamWarps] = sm.odd[joins & 1];       // a warp may be a join ahead of the readers
             if (lane == 0) any[w4] = odd;
