@@ -342,7 +342,9 @@ int gpt_attn_paged_append(const gpt_attn_paged_cache* cache, const void* k_new, 
  *             (0 for shapes the call rejects), 16-byte aligned, contents
  *             ignored on entry.  Calls that overlap on the GPU need one each.
  * What a node does not see does not reach it, infinities and NaN included.
- * Memory-bound up to some hundred rows N * H / Hkv per key head.  Errors as for
+ * With up to 16 rows N * H / Hkv per key head o is off by little more than its
+ * own rounding to bf16; with more the softmax weights are rounded to bf16 too,
+ * as in gpt_attn_fwd.  Memory-bound up to some hundred rows N * H / Hkv per key head.  Errors as for
  * gpt_attn_decode.  Asynchronous on `stream`.
  */
 size_t gpt_attn_paged_decode_workspace_bytes(int B, int H, int Hkv, int N, int D);
