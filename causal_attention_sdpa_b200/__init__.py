@@ -332,7 +332,14 @@ def _check_view(name, t, shape):
 
 
 def _strides(t):
-    return GptAttnStrides(t.stride(0), t.stride(1), t.stride(2))
+    return GptAttnStrides(*_steps(t))
+
+
+def _steps(t):
+    """Strides of the first three dimensions; one of size 1 is never stepped along, so its stride, which may be
+    anything, is 0."""
+    n, st = t.shape, t.stride()
+    return st[0] if n[0] > 1 else 0, st[1] if n[1] > 1 else 0, st[2] if n[2] > 1 else 0
 
 
 _STRIDES24 = ctypes.c_longlong * 24
@@ -346,8 +353,7 @@ def _layout(**tensors):
         return None
     v = []
     for t in ts:
-        st = t.stride()
-        v += (st[0], st[1], st[2])
+        v += _steps(t)
     return GptAttnLayout.from_buffer(_STRIDES24(*v))     # one flat copy; the struct keeps it alive
 
 
@@ -651,12 +657,10 @@ def _paged_cache(k_pages, v_pages, table, lens):
 
 
 def _pair_strides(a, b):
-    """Strides of two [b, h, n, d] tensors, or None when both are contiguous; a dimension of size 1
-    is never stepped along, so its stride does not matter."""
+    """Strides of two [b, h, n, d] tensors, or None when both are contiguous."""
     if a.is_contiguous() and b.is_contiguous():
         return None
-    return (GptAttnStrides * 2)(*[GptAttnStrides(*[t.stride(i) if t.shape[i] > 1 else 0 for i in range(3)])
-                                  for t in (a, b)])
+    return (GptAttnStrides * 2)(GptAttnStrides(*_steps(a)), GptAttnStrides(*_steps(b)))
 
 
 def gpt_attn_paged_append(k_pages, v_pages, table, lens, k_new, v_new, n_new=None, stream=None):

@@ -78,3 +78,36 @@ def test_paged_calls():
         out.append((a, b, *ga.gpt_attn_paged_decode(f(q), a, b, table, lens)))
     for x, y in zip(*out):
         assert torch.equal(x, y)
+
+
+def odd(t, dim):
+    """t with a stride of no use to anyone in its dimension of size 1."""
+    assert t.shape[dim] == 1
+    st = list(t.stride())
+    st[dim] = t.numel() + 3
+    return t.as_strided(t.shape, st)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("shape,dim", [((1, 3, 300), 0), ((2, 1, 300), 1), ((2, 3, 1), 2)], ids=["B1", "H1", "T1"])
+def test_strides_of_dimensions_of_size_one(D, shape, dim):
+    """They are never stepped along, so any will do, beside tensors that are not contiguous too."""
+    B, H, T = shape
+    q, k, v, do = (t.cuda() for t in make_inputs(B, H, T, D, seed=3))
+    major = lambda: torch.full((B, T, H, D), float("nan"), dtype=torch.bfloat16, device="cuda").transpose(1, 2)
+    for kw in (dict(), dict(window=60, sinks=5)):
+        fwd, bwd = (ga.gpt_attn_fwd_sinks, ga.gpt_attn_bwd_sinks) if kw else (ga.gpt_attn_fwd_ex, ga.gpt_attn_bwd_ex)
+        o, lse = fwd(q, k, v, **kw)
+        want = bwd(q, k, v, o, lse, do, **kw)
+        x = [odd(t, dim) for t in (q, k, v, o, do)]
+        got, l2 = fwd(*x[:3], o=odd(major(), dim), **kw)
+        assert torch.equal(got, o) and torch.equal(l2, lse)
+        g = bwd(*x[:4], lse, x[4], dq=major(), dk=odd(major(), dim), dv=odd(torch.empty_like(q), dim), **kw)
+        assert torch.equal(g[1], want[1]) and torch.equal(g[2], want[2])
+    assert ga.gpt_attn_check() == ga.GPT_ATTN_OK
+
+
+def test_prologue_strides_of_dimensions_of_size_one():
+    q, k, _, _ = (t.cuda() for t in make_inputs(1, 3, 300, 64, seed=3))
+    for a, b in zip(ga.gpt_attn_qk_prologue_fwd(odd(q, 0), odd(k, 0)), ga.gpt_attn_qk_prologue_fwd(q, k)):
+        assert torch.equal(a, b)
